@@ -19,6 +19,8 @@ Inference Engine", step 2):
 whose ``zeros`` are passed to dequantize_int4 / int4_matmul / int4_matmul_path
 as ``zeros=``; int4_linear(...) is one layer with fp16 or fp32 output, and
 ``dequantizing_gemm_amd.linear`` holds the Int4Linear module built on it.
+Int4Cache, int4_cache_write, int4_cache_read and int4_cache_attention keep a
+model's keys and values in the same codes (``dequantizing_gemm_amd.cache``).
 
 All tensors are torch tensors on the GPU; torch provides the device memory and
 the stream (work is enqueued on ``torch.cuda.current_stream()``). Every step of
@@ -36,7 +38,9 @@ import torch
 __all__ = ["quantize_int4", "quantize_int4_affine", "unpack_int4", "dequantize_int4", "int4_matmul",
            "int4_matmul_path", "int4_linear", "linear_workspace_bytes", "linear_workspace",
            "matmul_select",
-           "num_groups", "packed_bytes", "lib", "LIB_PATH", "Int4Error", "PATHS"]
+           "num_groups", "packed_bytes", "lib", "LIB_PATH", "Int4Error", "PATHS",
+           "Int4Cache", "int4_cache_write", "int4_cache_read", "int4_cache_attention",
+           "cache_attention_workspace_bytes", "cache_attention_workspace"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libint4dq.so")
 
@@ -339,3 +343,7 @@ def matmul_select(x, packed, scales, K, group=128) -> str:
     p = lib.int4_matmul_select(x.data_ptr(), xd, M, packed.data_ptr(), scales.data_ptr(), N, K,
                                group, 1)
     return PATH_NAMES.get(p, "invalid")
+
+
+from .cache import (Int4Cache, cache_attention_workspace, cache_attention_workspace_bytes,  # noqa: E402
+                    int4_cache_attention, int4_cache_read, int4_cache_write)

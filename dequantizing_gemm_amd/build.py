@@ -37,7 +37,8 @@ HIPFLAGS = [
 ]
 
 SOURCES = ["api.cpp", "quantize.hip", "unpack.hip", "dequantize.hip", "matmul_generic.hip",
-           "matmul_skinny.hip", "matmul_tiled.hip", "matmul_gemv.hip"]
+           "matmul_skinny.hip", "matmul_tiled.hip", "matmul_gemv.hip", "cache_api.cpp", "cache_store.hip",
+           "cache_attention.hip"]
 
 # The gemv kernels read their MFMA accumulators with VALU ops; selecting the
 # VGPR form of the MFMA instructions keeps the accumulators in VGPRs instead of

@@ -5,13 +5,12 @@
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
-#include <stdio.h>
-#include <stdarg.h>
 
 #include <mutex>
 
 #include "../../include/int4dq.h"
 #include "kernels.h"
+#include "status.h"
 
 // Scratch of int4_linear_noalloc: the workspace of a split of K for callers
 // that cannot allocate. Every GPU the library runs on holds its own copy, from
@@ -29,33 +28,10 @@ constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
 void* g_scratch_ptr[kMaxDevices] = {};         // device address of scratch, per device
 
-thread_local char g_err[512] = "";
-
-int fail(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-int ok() {
-  g_err[0] = '\0';
-  return INT4DQ_OK;
-}
-
-// a * b with overflow check into *out (both non-negative).
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > INT64_MAX / a) return false;
-  *out = a * b;
-  return true;
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return ok();
-  return fail(INT4DQ_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
+using int4dq::fail;
+using int4dq::hip_status;
+using int4dq::mul_ok;
+using int4dq::ok;
 
 // Shared validation of int4_matmul arguments; on success fills the sizes.
 int check_matmul(const void* x, int x_dtype, int64_t M, const uint8_t* packed,
@@ -265,7 +241,7 @@ int int4_matmul_select(const void* x, int x_dtype, int64_t M, const uint8_t* pac
   return choose_path(x, x_dtype, M, packed, N, K, group);
 }
 
-const char* int4_last_error(void) { return g_err; }
+const char* int4_last_error(void) { return int4dq::g_err; }
 
 }  // extern "C"
 
