@@ -36,16 +36,20 @@ HIPFLAGS = [
     "-Wall", "-Wno-unused-function",
 ]
 
+# The attention kernel's forms, a file for each width of a code row (longest first).
+ATTENTION_WIDTHS = [f"cache_attention_{n}.hip" for n in (256, 128, 192, 96, 64)]
+
 SOURCES = ["api.cpp", "quantize.hip", "unpack.hip", "dequantize.hip", "matmul_generic.hip",
            "matmul_skinny.hip", "matmul_tiled.hip", "matmul_gemv.hip", "cache_api.cpp", "cache_store.hip",
-           "cache_attention.hip"]
+           "cache_attention.hip", *ATTENTION_WIDTHS]
 
 # The gemv kernels read their MFMA accumulators with VALU ops; selecting the
 # VGPR form of the MFMA instructions keeps the accumulators in VGPRs instead of
 # AGPRs (no accvgpr read/write around them). The tiled kernel never touches its
 # accumulators inside the loop and keeps them in AGPRs, which leaves the VGPRs
 # to the operands.
-EXTRA = {"matmul_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
+# The attention kernel's scores pass from MFMA to VALU ops and back in the same way.
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=true"] for src in ["matmul_gemv.hip", *ATTENTION_WIDTHS]}
 
 
 # Every kernel's resource-usage remark is read back: a kernel that uses scratch
@@ -110,7 +114,7 @@ def build(verbose: bool = True) -> str:
     jobs = min(len(SOURCES) + 1, int(os.environ.get("MAX_JOBS", os.cpu_count() or 4)), 16)
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
         probes = [ex.submit(_compile, src) for src in PROBE_SRCS]
-        objs = list(ex.map(_compile, SOURCES))
+        objs = list(ex.map(_compile, [*ATTENTION_WIDTHS, *(s for s in SOURCES if s not in ATTENTION_WIDTHS)]))
         probe_objs = [f.result() for f in probes]
     _link(objs, LIB)
     _link(probe_objs, PROBE_LIB)

@@ -84,6 +84,7 @@ struct AttentionArgs {
   const void* q;
   int64_t q_row_stride, q_head_stride;
   int bf16;                 // q and out: 1 bfloat16, 0 binary16
+  int q_wide;               // every 8 channels of q lie 16-byte aligned and head_dim is a multiple of 8
   int ratio;                // query heads per key/value head
   float scale;
   int causal;

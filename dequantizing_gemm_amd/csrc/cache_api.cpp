@@ -77,6 +77,12 @@ bool strides_ok(int64_t row_stride, int64_t head_stride) {
   return row_stride >= -lim && row_stride <= lim && head_stride >= -lim && head_stride <= lim;
 }
 
+// The attention kernel's grid, a block of 256 threads for each 16 query rows of a
+// head and for each sequence and head, stays below 2^32 threads.
+bool call_fits(const RowsView& r, const CacheView& c, int64_t q_heads) {
+  return r.rows * q_heads <= (int64_t(1) << 27) && (int64_t)r.batch * c.heads <= (int64_t(1) << 22);
+}
+
 }  // namespace
 
 extern "C" {
@@ -129,9 +135,8 @@ int int4_cache_attention(const int4_cache_t* cache, const int4_cache_rows_t* row
     return fail(INT4DQ_EINVAL, "%s: dtype must be binary16 or bfloat16 (got %d)", fn, dtype);
   if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads)
     return fail(INT4DQ_EINVAL, "%s: q_heads must be a multiple of heads, up to 65535 (got %lld, %d)", fn, (ll)q_heads, c.heads);
-  int64_t t;
-  if (!mul_ok(r.rows, q_heads, &t) || t > INT32_MAX)
-    return fail(INT4DQ_EINVAL, "%s: rows * q_heads must be below 2^31", fn);
+  if (!call_fits(r, c, q_heads))
+    return fail(INT4DQ_EINVAL, "%s: rows * q_heads must be up to 2^27 and batch * heads up to 2^22", fn);
   if (!isfinite(scale) || !(scale > 0.0f))
     return fail(INT4DQ_EINVAL, "%s: scale must be finite and above 0 (got %g)", fn, (double)scale);
   if (window < 0 || (window > 0 && !causal))
@@ -143,7 +148,8 @@ int int4_cache_attention(const int4_cache_t* cache, const int4_cache_rows_t* row
   if ((uintptr_t)workspace % 256) return fail(INT4DQ_EINVAL, "%s: workspace must be 256-byte aligned", fn);
   if (r.rows == 0 || r.batch == 0) return ok();
   if (!q || !out) return fail(INT4DQ_EINVAL, "%s: q and out must be non-NULL", fn);
-  const AttentionArgs a{c, r, q, q_row_stride, q_head_stride, dtype == INT4DQ_ROWS_BF16 ? 1 : 0,
+  const bool wide = (uintptr_t)q % 16 == 0 && c.D % 8 == 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0;
+  const AttentionArgs a{c, r, q, q_row_stride, q_head_stride, dtype == INT4DQ_ROWS_BF16 ? 1 : 0, wide ? 1 : 0,
                         (int)(q_heads / c.heads), scale, causal ? 1 : 0, window, out, lse};
   return hip_status(int4dq::launch_cache_attention(a, workspace, workspace_bytes, (hipStream_t)stream),
                     "int4_cache_attention launch");
@@ -155,9 +161,8 @@ int64_t int4_cache_attention_workspace_bytes(const int4_cache_t* cache, const in
   CacheView c;
   RowsView r;
   if (check(fn, cache, rows, false, &c, &r) != INT4DQ_OK) return -1;
-  int64_t t;
-  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads || !mul_ok(r.rows, q_heads, &t) || t > INT32_MAX) {
-    fail(INT4DQ_EINVAL, "%s: q_heads must be a multiple of heads, with rows * q_heads below 2^31", fn);
+  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads || !call_fits(r, c, q_heads)) {
+    fail(INT4DQ_EINVAL, "%s: q_heads must be a multiple of heads, rows * q_heads up to 2^27, batch * heads up to 2^22", fn);
     return -1;
   }
   if (r.rows == 0 || r.batch == 0) return 0;

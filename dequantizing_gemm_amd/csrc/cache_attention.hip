@@ -1,111 +1,109 @@
 // cache_attention.hip -- softmax attention over the 4-bit cache
-// (include/int4dq_cache.h).
-//
-// One wavefront per (row, query head): 64 keys at a time, one a lane, their
-// scores in binary32 with the running maximum and sum of the softmax; then each
-// lane sums the values of its channels over those keys.
-#include "cache.h"
-#include "device_common.h"
+// (include/int4dq_cache.h): the plan of a call, and the kernel that joins the
+// partial results of tiles whose keys were shared out over several blocks. The
+// attention kernel itself is in cache_attention_kernel.h.
+#include "cache_attention_kernel.h"
 
 namespace int4dq {
 
 namespace {
 
-__device__ __forceinline__ float row_value(const void* p, int64_t i, int bf16) {
-  if (bf16) return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  return (float)static_cast<const _Float16*>(p)[i];
-}
+// out = sum_i exp2(m_i - M) o_i / sum_i exp2(m_i - M) l_i over the chunks of the
+// row's tile; one block for each (row, query head), blocks of rows that are
+// whole already leave at once. A channel quadruple a thread, the chunks dealt to
+// 256 / (8 C) groups of threads and joined through LDS.
+template <int C>
+__global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs a, Schedule sched,
+                                                                   const float* __restrict__ part) {
+  constexpr int T = 8 * C, GROUPS = 256 / T;
+  const int H = a.c.heads * a.ratio;
+  __shared__ __attribute__((aligned(16))) float4_t sums[GROUPS][T];
+  for (int64_t item = blockIdx.x; item < a.r.rows * H; item += gridDim.x) {
+    const int64_t t = item / H;
+    const int h = (int)(item % H), kh = h / a.ratio;
+    BlockWork work;
+    int first;
+    const bool got = find_sequence(
+        a, sched, [&](const SequenceWork& w, int, int, int) { return t >= w.first && t < w.first + w.rows; }, &work, &first);
+    if (!got || work.chunks == 1) continue;       // the same for the whole block
+    const int flat = (int)(t - work.w.first) * a.ratio + h % a.ratio;
+    const int tile = flat / sched.tile_rows, in_tile = flat % sched.tile_rows;
+    const int slot0 = work.slot + (work.w.tiles - 1 - tile) * work.chunks;
+    const int64_t size = partial_floats(sched.tile_rows, C), next = size * a.c.heads;
+    const float* const base = part + ((int64_t)slot0 * a.c.heads + kh) * size;
+    const float* const ml = base + (int64_t)sched.tile_rows * 32 * C + 2 * in_tile;
 
-__device__ __forceinline__ float code_value(uint32_t byte, int odd, const uint8_t* zeros, int64_t at) {
-  const uint32_t u = (byte >> (4 * odd)) & 15u;
-  return zeros ? (float)((int)u - (int)zeros[at]) : (float)sx4(u);
-}
+    const int lane = threadIdx.x & (kWave - 1);
+    float top = -1e30f;
+    for (int i = lane; i < work.chunks; i += kWave) top = __builtin_fmaxf(top, ml[i * next]);
+#pragma unroll
+    for (int x = 1; x < kWave; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+    float sum = 0.0f;
+    for (int i = lane; i < work.chunks; i += kWave)
+      sum += ml[i * next + 1] * __builtin_amdgcn_exp2f(ml[i * next] - top);
+#pragma unroll
+    for (int x = 1; x < kWave; x <<= 1) sum += __shfl_xor(sum, x);
 
-__global__ __launch_bounds__(64) void cache_attention_kernel(AttentionArgs a) {
-  const CacheView& c = a.c;
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, kh = h / a.ratio, DB = c.row_bytes();
-  int b;
-  int64_t pos;
-  if (!find_row(a.r, t, &b, &pos)) return;
-  int64_t hi = a.r.lengths[b];
-  if (a.causal && pos + 1 < hi) hi = pos + 1;
-  if (hi > a.r.max_pages << c.page_shift) hi = a.r.max_pages << c.page_shift;
-  const int64_t lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-  __shared__ float q[kMaxHeadDim], p[64];
-  __shared__ int64_t units[64];
-  for (int d = lane; d < c.D; d += 64) q[d] = row_value(a.q, t * a.q_row_stride + h * a.q_head_stride + d, a.bf16);
-  __syncthreads();
-  float m = -__builtin_inff(), l = 0.0f, o[kMaxHeadDim / 64] = {};
-  for (int64_t j0 = lo; j0 < hi; j0 += 64) {
-    const int64_t j = j0 + lane;
-    const int64_t page = j < hi ? find_page(a.r, c, b, j) : -1;
-    const int slot = (int)(j & (((int64_t)1 << c.page_shift) - 1)), ts = slot & 15;
-    const int64_t unit = page >= 0 ? c.unit(page, kh, slot) : -1;
-    float s = -__builtin_inff();
-    if (unit >= 0) {
-      float acc = 0.0f;
-      for (int d = 0; d < c.D; ++d) {
-        const int64_t at = (unit * c.G + d / c.group) * 16 + ts;
-        const uint32_t byte = c.k_packed[unit * 16 * DB + ts * DB + 4 * c.C * (d % 32 / 8) + 4 * (d / 32) + d % 8 / 2];
-        acc += q[d] * (code_value(byte, d % 2, c.k_zeros, at) * half_bits_to_float(c.k_scales[at]));
-      }
-      s = acc * a.scale;
-    }
-    float top = s;
-#pragma unroll
-    for (int x = 32; x > 0; x >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x));
-    top = __builtin_fmaxf(top, m);
-    if (top == -__builtin_inff()) continue;
-    const float alpha = expf(m - top), e = expf(s - top);
-    m = top;
-    float sum = e;
-#pragma unroll
-    for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
-    l = l * alpha + sum;
-    __syncthreads();
-    p[lane] = e;
-    units[lane] = unit;
-    __syncthreads();
-    for (int i = 0; i < kMaxHeadDim / 64; ++i) {
-      const int d = lane + 64 * i;
-      if (d >= c.D) break;
-      o[i] *= alpha;
-      for (int n = 0; n < 64; ++n) {
-        const int64_t un = units[n];
-        if (un < 0) continue;
-        const int tn = (int)((j0 + n) & 15);
-        const int64_t at = (un * c.G + d / c.group) * 16 + tn;
-        const uint32_t byte = c.v_packed[un * 16 * DB + (d / 2) * 16 + tn];
-        o[i] += p[n] * (code_value(byte, d % 2, c.v_zeros, at) * half_bits_to_float(c.v_scales[at]));
+    const int group = threadIdx.x / T, d = threadIdx.x % T * 4;
+    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (group < GROUPS) {
+#pragma unroll 4
+      for (int i = group; i < work.chunks; i += GROUPS) {
+        const float f = __builtin_amdgcn_exp2f(ml[i * next] - top);
+        v += *reinterpret_cast<const float4_t*>(base + i * next + in_tile * (32 * C) + d) * f;
       }
     }
-  }
-  const int H = c.heads * a.ratio;
-  for (int i = 0; i < kMaxHeadDim / 64; ++i) {
-    const int d = lane + 64 * i;
-    if (d >= c.D) break;
-    const float v = l > 0.0f ? o[i] / l : 0.0f;
-    const int64_t at = (t * H + h) * c.D + d;
-    if (a.bf16) {
-      const uint32_t u = __builtin_bit_cast(uint32_t, v);
-      static_cast<uint16_t*>(a.out)[at] = (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
-    } else {
-      static_cast<_Float16*>(a.out)[at] = (_Float16)v;
+    __syncthreads();                              // the item before is read
+    if (group < GROUPS) sums[group][threadIdx.x % T] = v;
+    __syncthreads();
+    if (threadIdx.x < T) {
+      v = sums[0][threadIdx.x];
+#pragma unroll
+      for (int i = 1; i < GROUPS; ++i) v += sums[i][threadIdx.x];
+      store_output(a, t * H + h, d, v * (sum == 0.0f ? 0.0f : 1.0f / sum));
     }
+    if (threadIdx.x == 0 && a.lse)
+      a.lse[t * H + h] = sum == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (top + __builtin_amdgcn_logf(sum));
   }
-  if (a.lse && lane == 0) a.lse[t * H + h] = l > 0.0f ? m + logf(l) : -__builtin_inff();
+}
+
+template <int C>
+hipError_t launch_width(const AttentionArgs& a, const Schedule& s, float* part, hipStream_t stream) {
+  hipError_t e = launch_attention_width<C>(a, s, part, stream);
+  if (e != hipSuccess || s.target == 0) return e;
+  hipLaunchKernelGGL(cache_attention_join_kernel<C>, dim3(stride_grid(a.r.rows * a.c.heads * a.ratio)), dim3(256), 0,
+                     stream, a, s, part);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_cache_attention(const AttentionArgs& a, void*, int64_t, hipStream_t stream) {
-  hipLaunchKernelGGL(cache_attention_kernel, dim3((unsigned)a.r.rows, (unsigned)(a.c.heads * a.ratio)), dim3(64), 0,
-                     stream, a);
-  return hipGetLastError();
+extern template hipError_t launch_attention_width<2>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+extern template hipError_t launch_attention_width<3>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+extern template hipError_t launch_attention_width<4>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+extern template hipError_t launch_attention_width<6>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+extern template hipError_t launch_attention_width<8>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+
+int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int ratio) {
+  const Schedule s = plan_of(c, r, ratio);
+  return workspace_slots(s) * c.heads * partial_floats(s.tile_rows, c.C) * 4;
 }
 
-int64_t cache_attention_workspace(const CacheView&, const RowsView&, int) { return 0; }
+hipError_t launch_cache_attention(const AttentionArgs& a, void* workspace, int64_t workspace_bytes,
+                                  hipStream_t stream) {
+  Schedule s = plan_of(a.c, a.r, a.ratio);
+  if (workspace_bytes < cache_attention_workspace(a.c, a.r, a.ratio)) {
+    s.units -= s.target;
+    s.target = 0;
+  }
+  float* const part = static_cast<float*>(workspace);
+  switch (a.c.C) {
+    case 2: return launch_width<2>(a, s, part, stream);
+    case 3: return launch_width<3>(a, s, part, stream);
+    case 4: return launch_width<4>(a, s, part, stream);
+    case 6: return launch_width<6>(a, s, part, stream);
+    default: return launch_width<8>(a, s, part, stream);
+  }
+}
 
 }  // namespace int4dq

@@ -1,0 +1,6 @@
+// cache_attention_128.hip -- the attention kernel for code rows of 128 channels.
+#include "cache_attention_launch.h"
+
+namespace int4dq {
+template hipError_t launch_attention_width<4>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+}

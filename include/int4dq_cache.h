@@ -138,7 +138,8 @@ int int4_cache_read(const int4_cache_t *cache, const int4_cache_rows_t *rows, vo
  * Preconditions not checked: q is finite and below 2^100 in magnitude.
  * Errors: those of int4_cache_write, and EINVAL for q_heads that is no multiple
  * of heads, a scale that is not finite and above 0, window < 0 or window
- * without causal, a bad workspace, INT4DQ_ROWS_F32.
+ * without causal, a bad workspace, INT4DQ_ROWS_F32, rows * q_heads above 2^27 or
+ * batch * heads above 2^22.
  */
 int int4_cache_attention(const int4_cache_t *cache, const int4_cache_rows_t *rows, const void *q,
                          int64_t q_row_stride, int64_t q_head_stride, int dtype, int64_t q_heads,
