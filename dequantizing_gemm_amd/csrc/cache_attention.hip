@@ -8,101 +8,96 @@ namespace int4dq {
 
 namespace {
 
-// out = sum_i exp2(m_i - M) o_i / sum_i exp2(m_i - M) l_i over the chunks of the
-// row's tile; one block for each (row, query head), blocks of rows that are
-// whole already leave at once. A channel quadruple a thread, the chunks dealt to
-// 256 / (8 C) groups of threads and joined through LDS.
+// out = sum_i exp2(m_i - M) o_i / sum_i exp2(m_i - M) l_i over the chunks of a
+// tile that was shared out, for each of its rows. One block for each slot and head
+// (those whose slot is no tile's first leave at once) and, in y, a few of the
+// tile's rows; a channel quadruple a thread, the chunks dealt to 256 / (8 C) groups
+// of threads and joined through LDS.
 template <int C>
-__global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs a, Schedule sched,
-                                                                   const float* __restrict__ part) {
+__global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
   constexpr int T = 8 * C, GROUPS = 256 / T;
-  const int H = a.c.heads * a.ratio;
+  const int slot = blockIdx.x / a.c.heads, kh = blockIdx.x % a.c.heads;
+  const PartRecord tile = ws.record[slot];          // read together with the count
+  if (slot >= *ws.used || tile.chunk != 0) return;
+  // starts that decrease can make more tiles than the grid has blocks, and leave
+  // this slot unwritten: whatever it holds then stays inside the arrays
+  if (tile.first < 0 || tile.flat0 < 0 || tile.flats < 0 || tile.chunks < 1 ||
+      tile.chunks > workspace_slots(sched) - slot || (int64_t)tile.first * a.ratio + tile.flats > a.r.rows * a.ratio)
+    return;
+  const int64_t size = partial_floats(sched.tile_rows, C), next = size * a.c.heads;
+  const float* const base = ws.part + ((int64_t)slot * a.c.heads + kh) * size;
+  const int lane = threadIdx.x & (kWave - 1), group = threadIdx.x / T, d = threadIdx.x % T * 4;
   __shared__ __attribute__((aligned(16))) float4_t sums[GROUPS][T];
-  for (int64_t item = blockIdx.x; item < a.r.rows * H; item += gridDim.x) {
-    const int64_t t = item / H;
-    const int h = (int)(item % H), kh = h / a.ratio;
-    BlockWork work;
-    int first;
-    const bool got = find_sequence(
-        a, sched, [&](const SequenceWork& w, int, int, int) { return t >= w.first && t < w.first + w.rows; }, &work, &first);
-    if (!got || work.chunks == 1) continue;       // the same for the whole block
-    const int flat = (int)(t - work.w.first) * a.ratio + h % a.ratio;
-    const int tile = flat / sched.tile_rows, in_tile = flat % sched.tile_rows;
-    const int slot0 = work.slot + (work.w.tiles - 1 - tile) * work.chunks;
-    const int64_t size = partial_floats(sched.tile_rows, C), next = size * a.c.heads;
-    const float* const base = part + ((int64_t)slot0 * a.c.heads + kh) * size;
-    const float* const ml = base + (int64_t)sched.tile_rows * 32 * C + 2 * in_tile;
-
-    const int lane = threadIdx.x & (kWave - 1);
+  for (int row = blockIdx.y; row < sched.tile_rows && tile.flat0 + row < tile.flats; row += gridDim.y) {
+    const float* const ml = base + (int64_t)sched.tile_rows * 32 * C + 2 * row;
     float top = -1e30f;
-    for (int i = lane; i < work.chunks; i += kWave) top = __builtin_fmaxf(top, ml[i * next]);
+    for (int i = lane; i < tile.chunks; i += kWave) top = __builtin_fmaxf(top, ml[i * next]);
 #pragma unroll
     for (int x = 1; x < kWave; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x));
     float sum = 0.0f;
-    for (int i = lane; i < work.chunks; i += kWave)
-      sum += ml[i * next + 1] * __builtin_amdgcn_exp2f(ml[i * next] - top);
-#pragma unroll
-    for (int x = 1; x < kWave; x <<= 1) sum += __shfl_xor(sum, x);
+    for (int i = lane; i < tile.chunks; i += kWave) sum += ml[i * next + 1] * __builtin_amdgcn_exp2f(ml[i * next] - top);
+    sum = lane_value(lane_scan(sum), kWave - 1);
 
-    const int group = threadIdx.x / T, d = threadIdx.x % T * 4;
     float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (group < GROUPS) {
 #pragma unroll 4
-      for (int i = group; i < work.chunks; i += GROUPS) {
+      for (int i = group; i < tile.chunks; i += GROUPS) {
         const float f = __builtin_amdgcn_exp2f(ml[i * next] - top);
-        v += *reinterpret_cast<const float4_t*>(base + i * next + in_tile * (32 * C) + d) * f;
+        v += *reinterpret_cast<const float4_t*>(base + i * next + row * (32 * C) + d) * f;
       }
+      sums[group][threadIdx.x % T] = v;
     }
-    __syncthreads();                              // the item before is read
-    if (group < GROUPS) sums[group][threadIdx.x % T] = v;
     __syncthreads();
+    const uint32_t flat = tile.flat0 + row, ratio = a.ratio;
+    const int64_t at = (int64_t)(tile.first + flat / ratio) * a.c.heads * ratio + kh * ratio + flat % ratio;
     if (threadIdx.x < T) {
       v = sums[0][threadIdx.x];
 #pragma unroll
       for (int i = 1; i < GROUPS; ++i) v += sums[i][threadIdx.x];
-      store_output(a, t * H + h, d, v * (sum == 0.0f ? 0.0f : 1.0f / sum));
+      store_output(a, at, d, v * (sum == 0.0f ? 0.0f : 1.0f / sum));
     }
     if (threadIdx.x == 0 && a.lse)
-      a.lse[t * H + h] = sum == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (top + __builtin_amdgcn_logf(sum));
+      a.lse[at] = sum == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (top + __builtin_amdgcn_logf(sum));
+    __syncthreads();                                 // the sums are read
   }
 }
 
 template <int C>
-hipError_t launch_width(const AttentionArgs& a, const Schedule& s, float* part, hipStream_t stream) {
-  hipError_t e = launch_attention_width<C>(a, s, part, stream);
+hipError_t launch_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream) {
+  hipError_t e = launch_attention_width<C>(a, s, ws, stream);
   if (e != hipSuccess || s.target == 0) return e;
-  hipLaunchKernelGGL(cache_attention_join_kernel<C>, dim3(stride_grid(a.r.rows * a.c.heads * a.ratio)), dim3(256), 0,
-                     stream, a, s, part);
+  const unsigned rows = (unsigned)(a.r.starts || a.ratio > 4 ? 4 : a.ratio);
+  hipLaunchKernelGGL(cache_attention_join_kernel<C>, dim3((unsigned)(workspace_slots(s) * a.c.heads), rows), dim3(256),
+                     0, stream, a, s, ws);
   return hipGetLastError();
 }
 
 }  // namespace
 
-extern template hipError_t launch_attention_width<2>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
-extern template hipError_t launch_attention_width<3>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
-extern template hipError_t launch_attention_width<4>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
-extern template hipError_t launch_attention_width<6>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
-extern template hipError_t launch_attention_width<8>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+extern template hipError_t launch_attention_width<2>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
+extern template hipError_t launch_attention_width<3>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
+extern template hipError_t launch_attention_width<4>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
+extern template hipError_t launch_attention_width<6>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
+extern template hipError_t launch_attention_width<8>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
 
 int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int ratio) {
   const Schedule s = plan_of(c, r, ratio);
-  return workspace_slots(s) * c.heads * partial_floats(s.tile_rows, c.C) * 4;
+  return s.target == 0 ? 0 : workspace_bytes(s, c.heads, c.C);
 }
 
-hipError_t launch_cache_attention(const AttentionArgs& a, void* workspace, int64_t workspace_bytes,
-                                  hipStream_t stream) {
+hipError_t launch_cache_attention(const AttentionArgs& a, void* workspace, int64_t bytes, hipStream_t stream) {
   Schedule s = plan_of(a.c, a.r, a.ratio);
-  if (workspace_bytes < cache_attention_workspace(a.c, a.r, a.ratio)) {
+  if (bytes < cache_attention_workspace(a.c, a.r, a.ratio)) {
     s.units -= s.target;
     s.target = 0;
   }
-  float* const part = static_cast<float*>(workspace);
+  const Workspace ws = workspace_at(workspace, s, a.c.heads, a.c.C);
   switch (a.c.C) {
-    case 2: return launch_width<2>(a, s, part, stream);
-    case 3: return launch_width<3>(a, s, part, stream);
-    case 4: return launch_width<4>(a, s, part, stream);
-    case 6: return launch_width<6>(a, s, part, stream);
-    default: return launch_width<8>(a, s, part, stream);
+    case 2: return launch_width<2>(a, s, ws, stream);
+    case 3: return launch_width<3>(a, s, ws, stream);
+    case 4: return launch_width<4>(a, s, ws, stream);
+    case 6: return launch_width<6>(a, s, ws, stream);
+    default: return launch_width<8>(a, s, ws, stream);
   }
 }
 

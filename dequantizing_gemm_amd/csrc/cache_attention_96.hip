@@ -2,5 +2,5 @@
 #include "cache_attention_launch.h"
 
 namespace int4dq {
-template hipError_t launch_attention_width<3>(const AttentionArgs&, const Schedule&, float*, hipStream_t);
+template hipError_t launch_attention_width<3>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
 }

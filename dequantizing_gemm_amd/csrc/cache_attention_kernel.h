@@ -94,16 +94,30 @@ __device__ __forceinline__ float rows_sum(float v) {
 
 struct BlockWork {
   int b, tile, chunk, chunks, slot;      // slot: of its partial result, where chunks > 1
-  int length;
   SequenceWork w;
 };
 
-// Every lane of the wavefront takes part; false if the block has no work.
-// `wanted(w, first)`: whether the sequence of this lane, whose blocks count from
-// `first`, is the one looked for (at most one is).
-template <typename Wanted>
-__device__ __forceinline__ bool find_sequence(const AttentionArgs& a, const Schedule& s, Wanted wanted, BlockWork* out,
-                                              int* first) {
+// Slots of partial results that the call uses in all.
+__device__ __forceinline__ int slots_used(const AttentionArgs& a, const Schedule& s) {
+  const int lane = threadIdx.x & (kWave - 1);
+  float all = 0.0f;
+  for (int b = lane; b < a.r.batch; b += kWave) {
+    const SequenceWork x = sequence_work(a, s.tile_rows, b);
+    all += (float)x.tiles * (float)x.steps;
+  }
+  const float each_step = blocks_per_step(s, lane_value(lane_scan(all), kWave - 1));
+  int slots = 0;
+  for (int b = lane; b < a.r.batch; b += kWave) {
+    const SequenceWork x = sequence_work(a, s.tile_rows, b);
+    const int chunks = chunks_of(x.steps, each_step);
+    if (chunks > 1) slots += chunks * x.tiles;
+  }
+  return lane_value(lane_scan(slots), kWave - 1);
+}
+
+// The share of block `unit` of its head; every lane of the wavefront takes part.
+// False if it has none.
+__device__ __forceinline__ bool find_block(const AttentionArgs& a, const Schedule& s, int unit, BlockWork* out) {
   const int lane = threadIdx.x & (kWave - 1);
   float all = 0.0f;
   SequenceWork w{};
@@ -112,46 +126,34 @@ __device__ __forceinline__ bool find_sequence(const AttentionArgs& a, const Sche
     all += (float)x.tiles * (float)x.steps;
     if (b < kWave) w = x;
   }
-  const int per = steps_per_block(s, lane_value(lane_scan(all), kWave - 1));
+  const float each_step = blocks_per_step(s, lane_value(lane_scan(all), kWave - 1));
   int blocks = 0, slots = 0;
   for (int b0 = 0; b0 < a.r.batch; b0 += kWave) {
     const int b = b0 + lane;
     int chunks = 0;
     if (b < a.r.batch) {
       if (b0 > 0) w = sequence_work(a, s.tile_rows, b);
-      chunks = chunks_of(w.steps, per);
+      chunks = chunks_of(w.steps, each_step);
     }
-    const int mine = chunks * w.tiles * (b < a.r.batch ? 1 : 0);
-    const int mine_slots = chunks > 1 ? mine : 0;
-    const int upto = lane_scan(mine);
-    const int slots_upto = lane_scan(mine_slots);
-    const uint64_t hit = __ballot(b < a.r.batch && mine > 0 && wanted(w, b, blocks + upto - mine, blocks + upto));
+    const int mine = b < a.r.batch ? chunks * w.tiles : 0, mine_slots = chunks > 1 ? mine : 0;
+    const int upto = blocks + lane_scan(mine), slots_upto = slots + lane_scan(mine_slots);
+    const uint64_t hit = __ballot(unit >= upto - mine && unit < upto);
     if (hit) {
       const int at = __builtin_ctzll(hit);
       out->b = b0 + at;
+      out->w = SequenceWork{lane_value(w.first, at), lane_value(w.end, at), lane_value(w.rows, at),
+                            lane_value(w.length, at), lane_value(w.keys, at), lane_value(w.tiles, at), 0};
       out->chunks = lane_value(chunks, at);
-      *first = lane_value(blocks + upto - mine, at);
-      out->slot = lane_value(slots + slots_upto - mine_slots, at);
-      out->w = sequence_work(a, s.tile_rows, out->b);
-      out->length = a.r.lengths[out->b];
+      const int i = unit - lane_value(upto - mine, at);
+      out->chunk = i % out->chunks;
+      out->tile = out->w.tiles - 1 - i / out->chunks;      // tiles that see most first
+      out->slot = lane_value(slots_upto - mine_slots, at) + i;
       return true;
     }
-    blocks += lane_value(upto, kWave - 1);
-    slots += lane_value(slots_upto, kWave - 1);
+    blocks = lane_value(upto, kWave - 1);
+    slots = lane_value(slots_upto, kWave - 1);
   }
   return false;
-}
-
-__device__ __forceinline__ bool find_block(const AttentionArgs& a, const Schedule& s, int unit, BlockWork* out) {
-  int first;
-  const bool got = find_sequence(
-      a, s, [&](const SequenceWork&, int, int from, int to) { return unit >= from && unit < to; }, out, &first);
-  if (!got) return false;
-  const int i = unit - first;
-  out->chunk = i % out->chunks;
-  out->tile = out->w.tiles - 1 - i / out->chunks;      // tiles that see most first
-  out->slot += (out->w.tiles - 1 - out->tile) * out->chunks + out->chunk;
-  return true;
 }
 
 // ---------------------------------------------------------------- operands
@@ -226,21 +228,7 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v) {
   return v;
 }
 
-// The 16-bit patterns of channels d0 .. d0 + 7 of the query that starts at
-// element `at`; those from `have` on are 0.
-__device__ __forceinline__ Words<4> load_query(const AttentionArgs& a, int64_t at, int have, int d0) {
-  const uint16_t* const p = static_cast<const uint16_t*>(a.q) + at + d0;
-  Words<4> r = {};
-  if (a.q_wide) {
-    if (have > 0) r = load_words<4>(reinterpret_cast<const uint8_t*>(p));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < have) r.w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
-  }
-  return r;
-}
-
+// Element e of 8 binary16 or bfloat16 patterns.
 __device__ __forceinline__ float query_value(const Words<4>& r, int e, int bf16) {
   const uint32_t h = e & 1 ? r.w[e / 2] >> 16 : r.w[e / 2] & 0xFFFFu;
   return bf16 ? __builtin_bit_cast(float, h << 16) : half_bits_to_float((uint16_t)h);
@@ -273,43 +261,169 @@ __device__ __forceinline__ void store_output(const AttentionArgs& a, int64_t row
 // C blocks of 32 channels, GC of them to a scale (scale_blocks), QT tiles of 16
 // query rows.
 template <int C, int GC, int QT, bool AFF>
-__global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, Schedule sched, float* part) {
+__global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
   constexpr int NG = C / GC, DB = 16 * C, TR = 16 * QT;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
   const int row = lane & 15, quarter = lane >> 4;
   const int heads = a.c.heads, kh = blockIdx.x % heads;
   BlockWork work;
+  if (sched.target > 0 && blockIdx.x == gridDim.x - 1 && wave == 0) {
+    const int used = slots_used(a, sched);
+    if (lane == 0) *ws.used = used;
+  }
   if (!find_block(a, sched, blockIdx.x / heads, &work)) return;
   const int flat0 = work.tile * TR, flats = work.w.rows * a.ratio;
+  if (work.chunks > 1 && kh == 0 && threadIdx.x == 0)
+    ws.record[work.slot] = PartRecord{work.w.first, flat0, flats, work.chunk, work.chunks, {}};
 
   // --- the tile's visible keys
+  const uint32_t ratio = (uint32_t)a.ratio;
   int lo_first, hi_first, lo_last, hi_last;
-  visible(a, work.w, work.length, flat0, &lo_first, &hi_first);
-  visible(a, work.w, work.length, (flat0 + TR < flats ? flat0 + TR : flats) - 1, &lo_last, &hi_last);
+  visible(a, work.w, (uint32_t)flat0 / ratio, &lo_first, &hi_first);
+  visible(a, work.w, ((flat0 + TR < flats ? flat0 + TR : flats) - 1) / ratio, &lo_last, &hi_last);
   int begin, end;
   chunk_steps(lo_first, hi_last, work.chunk, work.chunks, &begin, &end);
 
-  // --- queries: operand, factor of the scores, sums for the offsets
-  half8_t q[QT][C];
-  float factor[QT], qsum[QT][AFF ? NG : 1];
+  // --- queries: loads only; a row that the tile does not have reads the last one
+  Words<4> raw[QT][C];
   int lo[QT], hi[QT];
+  int64_t q_at[QT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     const int flat = flat0 + 16 * t + row;
-    const bool there = flat < flats;
-    lo[t] = hi[t] = 0;
-    if (there) visible(a, work.w, work.length, flat, &lo[t], &hi[t]);
-    const int64_t at = (work.w.first + (uint32_t)flat / (uint32_t)a.ratio) * a.q_row_stride +
-                       (int64_t)(kh * a.ratio + (uint32_t)flat % (uint32_t)a.ratio) * a.q_head_stride;
-    Words<4> raw[C];
+    const uint32_t f = flat < flats ? flat : flats - 1, token = f / ratio;
+    visible(a, work.w, token, &lo[t], &hi[t]);
+    if (flat >= flats) lo[t] = hi[t] = 0;
+    q_at[t] = (int64_t)(work.w.first + token) * a.q_row_stride + (int64_t)(kh * ratio + f % ratio) * a.q_head_stride;
+  }
+  if (a.q_wide) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int d = 32 * i + 8 * quarter;
+        raw[t][i] = load_words<4>(reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(a.q) + q_at[t] +
+                                                                   (d < a.c.D ? d : 0)));
+      }
+  } else {
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = 32 * i + 8 * quarter + 2 * e, last = a.c.D - 1;
+          const uint16_t* const p = static_cast<const uint16_t*>(a.q) + q_at[t];
+          raw[t][i].w[e] = p[d < last ? d : last] | (uint32_t)p[d + 1 < last ? d + 1 : last] << 16;
+        }
+  }
+
+  // --- loads of a step: the lane's key rows lie in the 16-token unit row / 4 of
+  // the step, its values and scales in unit `quarter`
+  typedef const int32_t __attribute__((address_space(4))) * ScalarPtr;         // read by scalar loads
+  const ScalarPtr table = (ScalarPtr)(uintptr_t)(a.r.table + (int64_t)work.b * a.r.table_stride);
+  const int key_off = ((row & 3) == 1 ? 2 : (row & 3) == 2 ? 1 : (row & 3)) * DB + quarter * 4 * C;
+  int group_of[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int x = NG == 1 ? 0 : g * GC * 32 / a.c.group;
+    group_of[g] = x < a.c.G ? x : a.c.G - 1;
+  }
+  // The 16-token units of the cache that hold the four of a step (0 where there is
+  // no page; bit u of `found` tells). Page numbers come through scalar loads, two
+  // steps ahead: as vector loads they would make the wait for them a wait for
+  // every load before them.
+  struct Units {
+    int at[4];
+    uint32_t found;
+  };
+  struct Pages {
+    int p[4];
+  };
+  const int page_units = heads << (a.c.page_shift - 4), head_unit = kh << (a.c.page_shift - 4);
+  const int last_index = (int)a.r.max_pages - 1, slots = (1 << a.c.page_shift) - 1;
+  auto pages_of = [&](int step) {
+    Pages r;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int index = (step * kStep + 16 * u) >> a.c.page_shift;
+      r.p[u] = table[index < last_index ? index : last_index];
+    }
+    return r;
+  };
+  auto units_of = [&](int step, const Pages& pages) {
+    Units r;
+    r.found = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool ok = (uint32_t)pages.p[u] < (uint32_t)a.c.pages;
+      r.at[u] = ok ? pages.p[u] * page_units + head_unit + (((step * kStep + 16 * u) & slots) >> 4) : 0;
+      r.found |= ok ? 1u << u : 0u;
+    }
+    return r;
+  };
+  auto pick = [&](const Units& x, int u) {
+    const int a0 = x.at[0], a1 = x.at[1], a2 = x.at[2], a3 = x.at[3];      // values: no address is selected
+    const int low = u & 1 ? a1 : a0, high = u & 1 ? a3 : a2;
+    return u & 2 ? high : low;
+  };
+  Words<C> kw[4];
+  Words<4> vw[C];
+  uint16_t ksc[NG], vsc[NG];             // of token `row` of the quarter's unit
+  uint8_t kz[AFF ? NG : 1];
+  Words<4> vz[AFF ? NG : 1];             // of the unit's 16 tokens
+  auto load_keys = [&](const Units& x) {
+    const int ku = pick(x, row >> 2), vu = pick(x, quarter);
+    const uint8_t* const p = a.c.k_packed + (int64_t)ku * (16 * DB) + key_off;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) kw[n] = load_words<C>(p + n * 4 * DB);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int64_t at = ((int64_t)vu * a.c.G + group_of[g]) * 16;
+      ksc[g] = a.c.k_scales[at + row];
+      if constexpr (AFF) kz[g] = a.c.k_zeros[at + row];
+    }
+  };
+  auto load_values = [&](const Units& x) {
+    const int vu = pick(x, quarter);
+    const uint8_t* const p = a.c.v_packed + (int64_t)vu * (16 * DB) + row * 16;
+#pragma unroll
+    for (int j = 0; j < C; ++j) vw[j] = load_words<4>(p + j * 256);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int64_t at = ((int64_t)vu * a.c.G + group_of[g]) * 16;
+      vsc[g] = a.c.v_scales[at + row];
+      if constexpr (AFF) vz[g] = load_words<4>(a.c.v_zeros + at);
+    }
+  };
+
+  int step = begin + wave;
+  Units units{};
+  Pages pages{};
+  if (step < end) {
+    units = units_of(step, pages_of(step));
+    pages = pages_of(step + 4);
+    load_keys(units);
+    load_values(units);
+  }
+
+  // --- queries: operand, factor of the scores, sums for affine codes
+  half8_t q[QT][C];
+  float factor[QT], qsum[QT][AFF ? NG : 1];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      raw[i] = load_query(a, at, there ? a.c.D - 32 * i - 8 * quarter : 0, 32 * i + 8 * quarter);
+    for (int i = 0; i < C; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(query_value(raw[i], e, a.bf16)));
-    }
+      for (int e = 0; e < 4; ++e) {
+        // channels from head_dim on, and rows that the tile does not have, are 0
+        const int have = flat0 + 16 * t + row < flats ? a.c.D - 32 * i - 8 * quarter - 2 * e : 0;
+        raw[t][i].w[e] &= have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u;
+        top = __builtin_fmaxf(top, __builtin_fabsf(query_value(raw[t][i], 2 * e, a.bf16)));
+        top = __builtin_fmaxf(top, __builtin_fabsf(query_value(raw[t][i], 2 * e + 1, a.bf16)));
+      }
     top = rows_max(top);
     // top * 2^up in [2^13, 2^14)
     const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
@@ -322,7 +436,7 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
       _Float16 h[8];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        h[n] = (_Float16)__builtin_ldexpf(query_value(raw[i], n, a.bf16), up);
+        h[n] = (_Float16)__builtin_ldexpf(query_value(raw[t][i], n, a.bf16), up);
         if constexpr (AFF) qsum[t][i / GC] += (float)h[n];
       }
       q[t][i] = half8_t{h[0], h[4], h[1], h[5], h[2], h[6], h[3], h[7]};
@@ -343,71 +457,11 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
     for (int j = 0; j < 2 * C; ++j) acc[t][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // --- loads of a step: the lane's key rows lie in the 16-token unit row / 4 of
-  // the step, its values and scales in unit `quarter`
-  const int32_t* const table = a.r.table + (int64_t)work.b * a.r.table_stride;
-  const int key_off = ((row & 3) == 1 ? 2 : (row & 3) == 2 ? 1 : (row & 3)) * DB + quarter * 4 * C;
-  int group_of[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const int x = NG == 1 ? 0 : g * GC * 32 / a.c.group;
-    group_of[g] = x < a.c.G ? x : a.c.G - 1;
-  }
-  const int64_t page_units = (int64_t)heads << (a.c.page_shift - 4), head_units = (int64_t)kh << (a.c.page_shift - 4);
-  // the cache's 16-token unit that holds unit u of a step, or -1
-  auto unit_of = [&](int step, int u) -> int64_t {
-    const int token = step * kStep + 16 * u;
-    const int index = token >> a.c.page_shift;
-    if (index >= a.r.max_pages) return -1;
-    const int page = table[index];
-    if (page < 0 || page >= a.c.pages) return -1;
-    return page * page_units + head_units + ((token & ((1 << a.c.page_shift) - 1)) >> 4);
-  };
-  Words<C> kw[4];
-  Words<4> vw[C];
-  uint16_t ksc[NG], vsc[NG];             // of token `row` of the quarter's unit
-  uint8_t kz[AFF ? NG : 1];
-  Words<4> vz[AFF ? NG : 1];             // of the unit's 16 tokens
-  bool there = false, there_next = false;
-  auto load_keys = [&](int64_t ku, int64_t vu) {
-    const uint8_t* const p = a.c.k_packed + ku * (16 * DB) + key_off;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) kw[n] = load_words<C>(p + n * 4 * DB);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int64_t at = (vu * a.c.G + group_of[g]) * 16;
-      ksc[g] = a.c.k_scales[at + row];
-      if constexpr (AFF) kz[g] = a.c.k_zeros[at + row];
-    }
-  };
-  auto load_values = [&](int64_t vu) {
-    const uint8_t* const p = a.c.v_packed + vu * (16 * DB) + row * 16;
-#pragma unroll
-    for (int j = 0; j < C; ++j) vw[j] = load_words<4>(p + j * 256);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int64_t at = (vu * a.c.G + group_of[g]) * 16;
-      vsc[g] = a.c.v_scales[at + row];
-      if constexpr (AFF) vz[g] = load_words<4>(a.c.v_zeros + at);
-    }
-  };
-
-  int step = begin + wave;
-  int64_t ku = -1, vu = -1;
-  if (step < end) {
-    ku = unit_of(step, row >> 2);
-    vu = unit_of(step, quarter);
-    there = vu >= 0;
-    load_keys(ku < 0 ? 0 : ku, vu < 0 ? 0 : vu);
-    load_values(vu < 0 ? 0 : vu);
-  }
   for (; step < end; step += 4) {
     const int next = step + 4;
-    if (next < end) {
-      ku = unit_of(next, row >> 2);
-      vu = unit_of(next, quarter);
-      there_next = vu >= 0;
-    }
+    const uint32_t found = units.found;
+    units = units_of(next, pages);
+    pages = pages_of(next + 4);
 
     // --- scores
     float s[QT][16], ks[NG], zk[AFF ? NG : 1];
@@ -430,14 +484,18 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float4_t dot = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (AFF)               // (8 - z) sum q
+            each<4>([&](auto ii) {
+              constexpr int i = decltype(ii)::value;
+              dot[i] = qsum[t][g] * of_token<token_of(4 * n + i)>(zk[g]);
+            });
 #pragma unroll
           for (int i = g * GC; i < (g + 1) * GC; ++i)
             dot = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i], q[t][i], dot, 0, 0, 0);
           each<4>([&](auto ii) {
             constexpr int i = decltype(ii)::value, tok = token_of(4 * n + i);
-            float d = dot[i];
-            if constexpr (AFF) d = __builtin_fmaf(of_token<tok>(zk[g]), qsum[t][g], d);
-            s[t][4 * n + i] = g == 0 ? d * of_token<tok>(ks[g]) : __builtin_fmaf(of_token<tok>(ks[g]), d, s[t][4 * n + i]);
+            const float x = dot[i] * of_token<tok>(ks[g]);
+            s[t][4 * n + i] = g == 0 ? x : s[t][4 * n + i] + x;
           });
         }
       }
@@ -451,12 +509,13 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
         for (int i = 0; i < C; ++i) asm volatile("" : "+v"(kw[n + 1].w[i]));
       }
     });
-    if (next < end) load_keys(ku < 0 ? 0 : ku, vu < 0 ? 0 : vu);
+    if (next < end) load_keys(units);
 
     // --- masks: only where a row does not see the whole step
     const int token0 = step * kStep + 16 * quarter;
-    const bool masked = step * kStep < lo_last || (step + 1) * kStep > hi_first || __ballot(!there) != 0;
+    const bool masked = step * kStep < lo_last || (step + 1) * kStep > hi_first || found != 15u;
     if (masked) {
+      const bool there = (found >> quarter) & 1u;
 #pragma unroll
       for (int t = 0; t < QT; ++t) {
         const int from = lo[t] - token0, to = there ? hi[t] - token0 : -1;
@@ -565,8 +624,7 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
         }
       }
     }
-    if (next < end) load_values(vu < 0 ? 0 : vu);
-    there = there_next;
+    if (next < end) load_values(units);
   }
 
   // --- join the block's wavefronts, 16 rows at a time. Lane (row, quarter) holds
@@ -611,8 +669,9 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
       for (int i = 0; i < 4; ++i) sum += ml[1][i][orow] * __builtin_amdgcn_exp2f(ml[0][i][orow] - mm);
       const bool whole = work.chunks == 1;
       const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-      const int64_t orow_at = (work.w.first + (uint32_t)flat / (uint32_t)a.ratio) * ((int64_t)heads * a.ratio) + kh * a.ratio + (uint32_t)flat % (uint32_t)a.ratio;
-      float* const slot = part + ((int64_t)work.slot * heads + kh) * partial_floats(TR, C);
+      const int64_t orow_at = (work.w.first + (uint32_t)flat / ratio) * ((int64_t)heads * ratio) + kh * ratio +
+                              (uint32_t)flat % ratio;
+      float* const slot = ws.part + ((int64_t)work.slot * heads + kh) * partial_floats(TR, C);
       for (int d = (tid & 15) * 4; d < 32 * C; d += 64) {
         float4_t v = *reinterpret_cast<const float4_t*>(&rows_out[0][orow][d]);
 #pragma unroll
@@ -637,6 +696,6 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
 // Defined for each width in a file of its own: launches the form for the cache's
 // groups and the schedule's tile height.
 template <int C>
-hipError_t launch_attention_width(const AttentionArgs& a, const Schedule& s, float* part, hipStream_t stream);
+hipError_t launch_attention_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream);
 
 }  // namespace int4dq

@@ -9,6 +9,7 @@
 // Test infrastructure: built and run only by tests/test_sanitize_cache_cpu.py.
 // Exit status 0 when every check holds.
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <random>
@@ -42,7 +43,7 @@ hipError_t launch_cache_attention(const AttentionArgs& a, void*, int64_t bytes, 
 }
 int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int ratio) {
   const Schedule s = plan_of(c, r, ratio);
-  return workspace_slots(s) * c.heads * partial_floats(s.tile_rows, c.C) * 4;
+  return s.target == 0 ? 0 : workspace_bytes(s, c.heads, c.C);
 }
 }  // namespace int4dq
 extern "C" const char* int4_last_error(void);
@@ -134,22 +135,33 @@ static void schedules() {
     a.causal = (int)pick(0, 1);
     a.window = a.causal && pick(0, 1) ? pick(1, 5000) : 0;
     Schedule s = plan_of(a.c, a.r, a.ratio);
-    CHECK(s.tile_rows == 16 || s.tile_rows == 32 || s.tile_rows == 64, "tile height");
+    CHECK(s.tile_rows == 16 || s.tile_rows == 32, "tile height");
     CHECK(s.tile_rows <= 16 * max_tiles(a.c.C, a.c.C / scale_blocks(a.c)), "a tile height that has a form");
     CHECK(a.c.C % scale_blocks(a.c) == 0 && (a.c.G == 1 || a.c.group % (32 * scale_blocks(a.c)) == 0), "blocks to a scale");
     if (trial % 5 == 4) { s.units -= s.target; s.target = 0; }
+    {
+      void* const p = malloc((size_t)workspace_bytes(s, a.c.heads, a.c.C));
+      const Workspace ws = workspace_at(p, s, a.c.heads, a.c.C);
+      *ws.used = 1;
+      if (s.target > 0) {
+        ws.record[0].chunk = ws.record[workspace_slots(s) - 1].chunks = 1;
+        ws.part[workspace_slots(s) * (a.c.heads * partial_floats(s.tile_rows, a.c.C)) - 1] = 1.0f;
+      }
+      free(p);
+    }
     double all = 0;
     for (int b = 0; b < B; ++b) {
       const SequenceWork w = sequence_work(a, s.tile_rows, b);
       all += (double)w.tiles * w.steps;
     }
     for (const double off : {1.0 - 3e-5, 1.0, 1.0 + 3e-5}) {     // binary32 sums in some order
-      const int per = steps_per_block(s, (float)(all * off));
+      const float per = blocks_per_step(s, (float)(all * off));
       int64_t blocks = 0, slots = 0, rows = 0;
       for (int b = 0; b < B; ++b) {
         const SequenceWork w = sequence_work(a, s.tile_rows, b);
         const int chunks = chunks_of(w.steps, per);
         blocks += (int64_t)w.tiles * chunks;
+        CHECK(chunks >= 1 && (s.target > 0 || chunks == 1), "chunks");
         if (chunks > 1) slots += (int64_t)w.tiles * chunks;
         rows += w.rows;
         CHECK(w.rows == 0 || (w.first >= 0 && w.first + w.rows <= a.r.rows), "rows inside the call");
@@ -158,8 +170,8 @@ static void schedules() {
         for (int t = 0; t < w.tiles; t += 1 + w.tiles / 3) {
           int lo, hi, lo1, hi1, at = -1, begin, end;
           const int last = ((t + 1) * s.tile_rows < flats ? (t + 1) * s.tile_rows : flats) - 1;
-          visible(a, w, lens[b], t * s.tile_rows, &lo, &hi);
-          visible(a, w, lens[b], last, &lo1, &hi1);
+          visible(a, w, t * s.tile_rows / a.ratio, &lo, &hi);
+          visible(a, w, last / a.ratio, &lo1, &hi1);
           CHECK(lo >= 0 && lo <= hi && lo <= lo1 && hi <= hi1 && hi1 <= w.keys, "visible keys in order");
           for (int k = 0; k < chunks; ++k) {
             chunk_steps(lo, hi1, k, chunks, &begin, &end);
