@@ -28,7 +28,7 @@ import ctypes
 
 import torch
 
-from . import _gpu, _raise, _stream, lib
+from . import _gpu, _raise, lib
 
 __all__ = ["Int4Cache", "int4_cache_write", "int4_cache_read", "int4_cache_attention",
            "cache_attention_workspace_bytes", "cache_attention_workspace"]
@@ -60,6 +60,13 @@ CACHE_SIGNATURES = {
 for _name, (_res, _args) in CACHE_SIGNATURES.items():
     _fn = getattr(lib, _name)
     _fn.restype, _fn.argtypes = _res, _args
+
+
+try:                                    # a quarter of the time of current_stream(device).cuda_stream
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 class Int4Cache:
@@ -140,30 +147,32 @@ class Int4Cache:
                                                           self.v_scales, self.v_zeros) if t is not None)
 
 
+def _int32(cache, name, t, ndim):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != ndim:
+        raise ValueError(f"{name} must be an int32 tensor of {ndim} dimension(s)")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on {cache.device} (got {t.device})")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
 def _plan(cache, page_table, lengths, starts, rows):
     """The rows descriptor, checked; rows: what the row-wise arrays hold."""
     if not isinstance(cache, Int4Cache):
         raise ValueError("cache must be an Int4Cache")
-    for name, t, ndim in (("page_table", page_table, 2), ("lengths", lengths, 1), ("starts", starts, 1)):
-        if t is None and name == "starts":
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != ndim:
-            raise ValueError(f"{name} must be an int32 tensor of {ndim} dimension(s)")
-        if t.device != cache.device:
-            raise ValueError(f"{name} must be on {cache.device} (got {t.device})")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
+    _int32(cache, "page_table", page_table, 2)
+    _int32(cache, "lengths", lengths, 1)
     batch, max_pages = page_table.shape
     if lengths.shape[0] != batch:
         raise ValueError(f"lengths has {lengths.shape[0]} entries, page_table {batch} rows")
+    sp = None
     if starts is not None:
+        _int32(cache, "starts", starts, 1)
         if starts.shape[0] != batch + 1:
             raise ValueError(f"starts has {starts.shape[0]} entries, a batch of {batch} needs {batch + 1}")
         sp = starts.data_ptr()
     elif rows != batch:
         raise ValueError(f"without starts there is one row a sequence (got {rows} rows, {batch} sequences)")
-    else:
-        sp = None
     stride = page_table.stride(0) if batch > 1 else max_pages
     if stride < max_pages:
         raise ValueError("page_table rows must not overlap")
@@ -171,32 +180,30 @@ def _plan(cache, page_table, lengths, starts, rows):
 
 
 def _rows_array(cache, t, name, heads):
-    """Checks a [rows, heads, head_dim] tensor with channels side by side; its strides."""
+    """Checks a [rows, heads, head_dim] tensor with channels side by side; its row
+    and head strides."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.head_dim:
         raise ValueError(f"{name} must be a tensor [rows, {heads}, {cache.head_dim}]"
                          + (f" (got {tuple(t.shape)})" if isinstance(t, torch.Tensor) else ""))
     if t.device != cache.device:
         raise ValueError(f"{name} must be on {cache.device} (got {t.device})")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    row, head, channel = t.stride()
+    if channel != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t.stride(0), t.stride(1)
+    return row, head
 
 
-class _on:
-    """Makes a device current for a call, where it is not already."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, device):
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(cache, fn, what, *args):
+    """Calls a C entry point with the cache's device current, on that device's
+    current stream; a status other than OK is raised."""
+    index = cache.device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(cache._ref, *args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(cache._ref, *args, _raw_stream(index))
+    if rc:
+        _raise(rc, what)
 
 
 def int4_cache_write(cache: Int4Cache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
@@ -208,12 +215,9 @@ def int4_cache_write(cache: Int4Cache, k: torch.Tensor, v: torch.Tensor, page_ta
         raise ValueError(f"k and v must be float32, float16 or bfloat16, both the same (got {k.dtype}, {v.dtype})")
     if v.shape[0] != k.shape[0]:
         raise ValueError(f"k has {k.shape[0]} rows, v {v.shape[0]}")
-    rows = _plan(cache, page_table, lengths, starts, k.shape[0])
-    with _on(cache.device):
-        rc = lib.int4_cache_write(cache._ref, ctypes.addressof(rows), k.data_ptr(), *ks, v.data_ptr(), *vs,
-                                  ROWS_DTYPES[k.dtype], _stream(k))
-    if rc:
-        _raise(rc, "int4_cache_write")
+    plan = _plan(cache, page_table, lengths, starts, k.shape[0])
+    _call(cache, lib.int4_cache_write, "int4_cache_write", ctypes.addressof(plan), k.data_ptr(), *ks, v.data_ptr(), *vs,
+          ROWS_DTYPES[k.dtype])
 
 
 def int4_cache_read(cache: Int4Cache, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -232,18 +236,14 @@ def int4_cache_read(cache: Int4Cache, page_table: torch.Tensor, lengths: torch.T
     plan = _plan(cache, page_table, lengths, starts, rows)
     shape = (rows, cache.heads, cache.head_dim)
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=cache.device),
-               torch.empty(shape, dtype=dtype, device=cache.device))
+        out = torch.empty((2, *shape), dtype=dtype, device=cache.device).unbind(0)
     else:
         for name, t in zip(("out[0]", "out[1]"), out):
             _gpu(t, name, dtype, 3)
             if tuple(t.shape) != shape or t.device != cache.device:
                 raise ValueError(f"{name} must be {shape} on {cache.device}")
-    with _on(cache.device):
-        rc = lib.int4_cache_read(cache._ref, ctypes.addressof(plan), out[0].data_ptr(), out[1].data_ptr(),
-                                 ROWS_DTYPES[dtype], _stream(out[0]))
-    if rc:
-        _raise(rc, "int4_cache_read")
+    _call(cache, lib.int4_cache_read, "int4_cache_read", ctypes.addressof(plan), out[0].data_ptr(), out[1].data_ptr(),
+          ROWS_DTYPES[dtype])
     return out
 
 
@@ -291,7 +291,7 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
     rows = q.shape[0]
     plan = _plan(cache, page_table, lengths, starts, rows)
     if out is None:
-        out = torch.empty((rows, q_heads, cache.head_dim), dtype=q.dtype, device=q.device)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
         _gpu(out, "out", q.dtype, 3)
         if tuple(out.shape) != tuple(q.shape) or out.device != q.device:
@@ -306,11 +306,7 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
         if workspace.device != q.device:
             raise ValueError(f"workspace must be on {q.device}")
         n = workspace.numel()
-    with _on(cache.device):
-        rc = lib.int4_cache_attention(cache._ref, ctypes.addressof(plan), q.data_ptr(), *qs, ROWS_DTYPES[q.dtype],
-                                      q_heads, cache.head_dim ** -0.5 if scale is None else scale, bool(causal),
-                                      int(window), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                      workspace.data_ptr() if n else None, n, _stream(q))
-    if rc:
-        _raise(rc, "int4_cache_attention")
+    _call(cache, lib.int4_cache_attention, "int4_cache_attention", ctypes.addressof(plan), q.data_ptr(), *qs,
+          ROWS_DTYPES[q.dtype], q_heads, cache.head_dim ** -0.5 if scale is None else scale, bool(causal), int(window),
+          out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr() if n else None, n)
     return (out, lse) if return_lse else out

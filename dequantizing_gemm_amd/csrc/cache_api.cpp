@@ -42,9 +42,10 @@ int check(const char* fn, const int4_cache_t* c, const int4_cache_rows_t* r, boo
     return fail(INT4DQ_EINVAL, "%s: sizes overflow int64", fn);
   if (c->pages * c->heads * (c->page_size / 16) > INT32_MAX)     // at least 2 TiB of codes
     return fail(INT4DQ_EINVAL, "%s: the cache must hold fewer than 2^31 units of 16 tokens and one head", fn);
-  if (r->batch < 0 || r->batch > (1 << 24))
-    return fail(INT4DQ_EINVAL, "%s: batch must be 0 to 2^24 (got %lld)", fn, (ll)r->batch);
-  if (r->rows < 0 || r->rows > (1 << 26))     // 256 threads for 8 rows: grids below 2^32 threads
+  // a block of 256 threads for 64 rows and two for a sequence: grids below 2^32 threads
+  if (r->batch < 0 || r->batch > (1 << 22))
+    return fail(INT4DQ_EINVAL, "%s: batch must be 0 to 2^22 (got %lld)", fn, (ll)r->batch);
+  if (r->rows < 0 || r->rows > (1 << 26))
     return fail(INT4DQ_EINVAL, "%s: rows must be 0 to 2^26 (got %lld)", fn, (ll)r->rows);
   if (!r->starts && r->rows != r->batch)
     return fail(INT4DQ_EINVAL, "%s: without starts there is one row a sequence (got %lld rows, %lld sequences)", fn,

@@ -149,8 +149,9 @@ inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   s.target = (resident * kComputeUnits + c.heads - 1) / c.heads;
   s.share = 1.001f / (float)s.target;
   s.min_steps = 4;
-  // no tile has more steps than the page table holds: none to share out
-  if ((r.max_pages << c.page_shift) <= s.min_steps * kStep) s.target = 0;
+  // Where the page table holds at most 1024 tokens a sequence, every tile is left
+  // to one block (4 steps a wavefront) and the join kernel's launch is saved.
+  if ((r.max_pages << c.page_shift) <= 16 * kStep) s.target = 0;
   s.units = (int)(s.target + r.rows * ratio / s.tile_rows + r.batch);
   return s;
 }

@@ -2,13 +2,21 @@
 // them back (include/int4dq_cache.h).
 //
 // Mathematics: the group quantizer of quantize.hip on rows of head_dim
-// channels, one row per (token, head) of the keys and of the values.
+// channels, one row per (token, head) of the keys and of the values. Bound by
+// memory.
 //
-// Work decomposition: a lane owns 8 channels of a row, LP lanes a row (the
-// power of two that holds 4 C), 256 threads a block of 16 or more consecutive
-// rows of one head, blockIdx.z the keys or the values. A group's extremes are
-// a DPP butterfly over its lanes. A lane's 8 key codes are 4 adjacent bytes of
-// the token's row; its 8 value codes lie in 4 byte rows of the token's unit.
+// Work decomposition: a block of 256 threads takes 64 positions (a step: four of
+// the cache's 16-token units) of one head of one sequence, blockIdx.z the keys
+// or the values. For quantising, thread 4 t + a owns channels 32 i + 8 a .. + 7 of
+// token t for all i: its key codes are then 4 C adjacent bytes of the cache, and
+// a group's extremes are the thread's own and a DPP butterfly over the token's four
+// threads. Value codes, whose bytes lie a token apart, go through LDS and leave as
+// 16-byte rows of a unit; a unit of which some tokens are not written (a run's
+// ragged ends) leaves byte by byte. Reading back, a thread takes 4 C bytes of a
+// token's key row, or one 16-token byte row of the values (two channels of 16
+// tokens), so that a wavefront's stores cover whole rows.
+#include <type_traits>
+
 #include "cache.h"
 #include "quantize_common.h"
 
@@ -18,167 +26,346 @@ namespace int4dq {
 
 namespace {
 
-template <int DT>
-__device__ __forceinline__ float load_row(const void* p, int64_t i) {
-  if constexpr (DT == INT4DQ_ROWS_F32) return static_cast<const float*>(p)[i];
-  else if constexpr (DT == INT4DQ_ROWS_F16) return (float)static_cast<const _Float16*>(p)[i];
-  else return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-}
-
-// Round to nearest even; the values here are finite.
-__device__ __forceinline__ uint16_t bf16_bits(float v) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
-}
-
-template <int DT>
-__device__ __forceinline__ void store_row(void* p, int64_t i, float v) {
-  if constexpr (DT == INT4DQ_ROWS_F32) static_cast<float*>(p)[i] = v;
-  else if constexpr (DT == INT4DQ_ROWS_F16) static_cast<_Float16*>(p)[i] = (_Float16)v;
-  else static_cast<uint16_t*>(p)[i] = bf16_bits(v);
-}
-
+// Keys or values in the caller's arrays: what a launch takes.
 struct RowArray {
-  const void* p;
+  void* p;
   int64_t row_stride, head_stride;
+  int wide;                  // 8 channels lie 16-byte aligned (binary32: 32 bytes from a 16-byte boundary)
 };
 
-template <int DT, int LP, int LANES, bool AFF>
-__global__ __launch_bounds__(256) void cache_write_kernel(CacheView c, RowsView r, RowArray k, RowArray v) {
-  const int rl = threadIdx.x / LP, lane = threadIdx.x % LP;
-  const int head = blockIdx.y;
-  const bool keys = blockIdx.z == 0;
-  const RowArray in = keys ? k : v;
-  uint8_t* const packed = keys ? c.k_packed : c.v_packed;
-  uint16_t* const scales = keys ? c.k_scales : c.v_scales;
-  uint8_t* const zeros = keys ? c.k_zeros : c.v_zeros;
-  const int64_t t = (int64_t)blockIdx.x * (256 / LP) + rl;
-  int b;
-  int64_t pos, page = -1;
-  if (t < r.rows && find_row(r, t, &b, &pos)) page = find_page(r, c, b, pos);
-  const int d0 = lane * 8;
-  float x[8];
+// ---------------------------------------------------------------- the block's share
+
+// 64 positions from `base` of sequence b; its rows start at position p0 with row
+// `first` of the call, `rows` of them.
+struct StoreBlock {
+  int b, first, rows;
+  int64_t p0, base;
+};
+
+__device__ __forceinline__ int lane_sum_upto(int v) {          // inclusive, over the wavefront
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    x[e] = page >= 0 && d0 + e < c.D ? load_row<DT>(in.p, t * in.row_stride + head * in.head_stride + d0 + e) : 0.0f;
-  uint32_t word = 0, zp = 0;
-  _Float16 s16;
-  if constexpr (!AFF) {
-    float amax = 0.0f;
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int x = __shfl_up(v, o);
+    if ((int)(threadIdx.x & (kWave - 1)) >= o) v += x;
+  }
+  return v;
+}
+
+__device__ __forceinline__ StoreBlock store_rows(const RowsView& r, int b) {
+  const int s0 = r.starts ? r.starts[b] : b, s1 = r.starts ? r.starts[b + 1] : b + 1;
+  StoreBlock x;
+  x.b = b;
+  x.first = s0 > 0 ? s0 : 0;
+  const int last = s1 < r.rows ? s1 : (int)r.rows;
+  x.rows = last > x.first ? last - x.first : 0;
+  x.p0 = (int64_t)r.lengths[b] - s1 + x.first;
+  x.base = (x.p0 >> 6) << 6;
+  return x;
+}
+
+// Steps that a sequence's rows touch. Over a batch they number at most
+// rows / 64 + 2 batch, the grid's size; without starts, one row touches one.
+__device__ __forceinline__ int store_steps(const StoreBlock& x) {
+  return x.rows > 0 ? (int)(((x.p0 + x.rows - 1) >> 6) - (x.p0 >> 6)) + 1 : 0;
+}
+
+__device__ __forceinline__ bool find_store_block(const RowsView& r, int unit, StoreBlock* out) {
+  if (!r.starts) {
+    *out = store_rows(r, unit);
+    return true;
+  }
+  const int lane = threadIdx.x & (kWave - 1);
+  int before = 0;
+  for (int b0 = 0; b0 < r.batch; b0 += kWave) {
+    const int steps = b0 + lane < r.batch ? store_steps(store_rows(r, b0 + lane)) : 0;
+    const int upto = before + lane_sum_upto(steps);
+    const uint64_t hit = __ballot(unit >= upto - steps && unit < upto);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      *out = store_rows(r, b0 + at);
+      out->base += (int64_t)(unit - __builtin_amdgcn_readlane(upto - steps, at)) * 64;
+      return true;
+    }
+    before = __builtin_amdgcn_readlane(upto, kWave - 1);
+  }
+  return false;
+}
+
+// ---------------------------------------------------------------- elements
+
+template <int DT>
+using Bits = typename std::conditional<DT == INT4DQ_ROWS_F32, uint32_t, uint16_t>::type;
+
+template <int DT>
+__device__ __forceinline__ float value_of(Bits<DT> v) {
+  if constexpr (DT == INT4DQ_ROWS_F32) return __builtin_bit_cast(float, v);
+  else if constexpr (DT == INT4DQ_ROWS_F16) return half_bits_to_float(v);
+  else return __builtin_bit_cast(float, (uint32_t)v << 16);
+}
+
+// Rounded to nearest even; bfloat16 for finite values and infinities.
+template <int DT>
+__device__ __forceinline__ Bits<DT> bits_of(float v) {
+  if constexpr (DT == INT4DQ_ROWS_F32) return __builtin_bit_cast(uint32_t, v);
+  else if constexpr (DT == INT4DQ_ROWS_F16) return __builtin_bit_cast(uint16_t, (_Float16)v);
+  else {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+  }
+}
+
+// N adjacent elements from or to memory that is aligned to all of them (at most 16 bytes).
+template <typename T, int N>
+struct __attribute__((aligned(N * sizeof(T) < 16 ? N * sizeof(T) : 16))) Pack {
+  T v[N];
+};
+
+// ---------------------------------------------------------------- write
+
+template <int DT, int C, bool AFF>
+__global__ __launch_bounds__(256) void cache_write_kernel(CacheView c, RowsView r, RowArray keys, RowArray values) {
+  constexpr int DB = 16 * C;
+  StoreBlock w;
+  if (!find_store_block(r, blockIdx.x, &w)) return;
+  const int head = blockIdx.y, tid = threadIdx.x, token = tid >> 2, a = tid & 3;
+  const bool is_keys = blockIdx.z == 0;
+  const RowArray in = is_keys ? keys : values;
+  uint8_t* const packed = is_keys ? c.k_packed : c.v_packed;
+  uint16_t* const scales = is_keys ? c.k_scales : c.v_scales;
+  uint8_t* const zeros = is_keys ? c.k_zeros : c.v_zeros;
+
+  const int64_t pos = w.base + token, at_row = pos - w.p0;
+  const int64_t page = at_row >= 0 && at_row < w.rows ? find_page(r, c, w.b, pos) : -1;
+  const bool there = page >= 0;
+
+  // --- the thread's channels, 0 where there are none
+  Bits<DT> raw[C][8];
+  const Bits<DT>* const src = static_cast<const Bits<DT>*>(in.p) + (w.first + (there ? at_row : 0)) * in.row_stride +
+                              head * in.head_stride;
+  if (in.wide) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[e]));
-    s16 = (_Float16)(run_umax_bits<LANES>(amax) / 7.0f);
-    const float sf = (float)s16, rsf = scale_rcp(sf);
+    for (int i = 0; i < C; ++i) {
+      const int d = 32 * i + 8 * a;
+      const bool have = there && d < c.D;            // head_dim is a multiple of 8
+      const auto v = *reinterpret_cast<const Pack<Bits<DT>, 8>*>(src + (have ? d : 0));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) word |= code_of(x[e], sf, rsf) << (4 * e);
+      for (int e = 0; e < 8; ++e) raw[i][e] = have ? v.v[e] : (Bits<DT>)0;
+    }
   } else {
-    float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = 32 * i + 8 * a + e;
+        const bool have = there && d < c.D;
+        const Bits<DT> v = src[have ? d : 0];
+        raw[i][e] = have ? v : (Bits<DT>)0;
+      }
+  }
+
+  // --- extremes of each block of 32 channels, then of each group
+  float lo[C], hi[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    lo[i] = hi[i] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      lo = __builtin_fminf(lo, x[e]);
-      hi = __builtin_fmaxf(hi, x[e]);
+      const float x = value_of<DT>(raw[i][e]);
+      if constexpr (AFF) lo[i] = __builtin_fminf(lo[i], x);
+      hi[i] = __builtin_fmaxf(hi[i], AFF ? x : __builtin_fabsf(x));
     }
-    lo = run_umax_bits<LANES>(lo);
-    hi = run_umax_bits<LANES>(hi);
-    s16 = (_Float16)((hi - lo) / 15.0f);
-    const float sf = (float)s16, rsf = scale_rcp(sf);
-    zp = affine_zp(lo, sf);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (d0 + e < c.D) word |= affine_code(x[e], sf, rsf, zp) << (4 * e);
+    if constexpr (AFF) lo[i] = run_umax_bits<4>(lo[i]);
+    hi[i] = run_umax_bits<4>(hi[i]);
   }
-  if (page < 0 || lane >= 4 * c.C) return;
-  const int slot = (int)(pos & (((int64_t)1 << c.page_shift) - 1));
+  const int blocks = c.G == 1 ? C : c.group / 32;    // of 32 channels, to a group
+  uint32_t word[C];
+  const int slot = (int)(pos & (((int64_t)1 << c.page_shift) - 1)), ts = slot & 15;
   const int64_t unit = c.unit(page, head, slot);
-  const int DB = c.row_bytes(), ts = slot & 15;
-  if (keys) {
-    const int64_t at = unit * 16 * DB + ts * DB + (lane & 3) * 4 * c.C + (lane >> 2) * 4;
-    *reinterpret_cast<uint32_t*>(packed + at) = word;
-  } else {
-    uint8_t* const at = packed + unit * 16 * DB + (int64_t)lane * 64 + ts;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) at[16 * j] = (uint8_t)(word >> (8 * j));
-  }
-  if (lane % LANES == 0 && d0 < c.D) {
-    const int64_t at = (unit * c.G + lane / LANES) * 16 + ts;
-    scales[at] = __builtin_bit_cast(uint16_t, s16);
-    if constexpr (AFF) zeros[at] = (uint8_t)zp;
-  }
-}
-
-template <int DT, int LP>
-__global__ __launch_bounds__(256) void cache_read_kernel(CacheView c, RowsView r, void* k, void* v) {
-  const int rl = threadIdx.x / LP, lane = threadIdx.x % LP;
-  const int head = blockIdx.y;
-  const bool keys = blockIdx.z == 0;
-  const int64_t t = (int64_t)blockIdx.x * (256 / LP) + rl;
-  int b;
-  int64_t pos;
-  const int d0 = lane * 8;
-  if (t >= r.rows || d0 >= c.D || !find_row(r, t, &b, &pos)) return;
-  void* const out = keys ? k : v;
-  const int64_t o = (t * c.heads + head) * c.D + d0;
-  const int64_t page = find_page(r, c, b, pos);
-  uint32_t word = 0, zp = 0;
-  float s = 0.0f;
-  const uint8_t* const zeros = keys ? c.k_zeros : c.v_zeros;
-  if (page >= 0) {
-    const int slot = (int)(pos & (((int64_t)1 << c.page_shift) - 1));
-    const int64_t unit = c.unit(page, head, slot);
-    const int DB = c.row_bytes(), ts = slot & 15;
-    if (keys) {
-      const int64_t at = unit * 16 * DB + ts * DB + (lane & 3) * 4 * c.C + (lane >> 2) * 4;
-      word = *reinterpret_cast<const uint32_t*>(c.k_packed + at);
-    } else {
-      const uint8_t* const at = c.v_packed + unit * 16 * DB + (int64_t)lane * 64 + ts;
+  for (int i = 0; i < C; ++i) {
+    const int g = blocks == C ? 0 : i / blocks, from = g * blocks;
+    float top = 0.0f, bottom = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) word |= (uint32_t)at[16 * j] << (8 * j);
+    for (int k = 0; k < C; ++k)
+      if (k >= from && k < from + blocks) {
+        top = __builtin_fmaxf(top, hi[k]);
+        if constexpr (AFF) bottom = __builtin_fminf(bottom, lo[k]);
+      }
+    const _Float16 s16 = (_Float16)(AFF ? (top - bottom) / 15.0f : top / 7.0f);
+    const float sf = (float)s16, rsf = scale_rcp(sf);
+    const uint32_t zp = AFF ? affine_zp(bottom, sf) : 0u;
+    word[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = value_of<DT>(raw[i][e]);
+      const uint32_t u = AFF ? affine_code(x, sf, rsf, zp) : code_of(x, sf, rsf);
+      // padding channels have code 0
+      if (!AFF || 32 * i + 8 * a + e < c.D) word[i] |= u << (4 * e);
     }
-    const int64_t at = (unit * c.G + d0 / c.group) * 16 + ts;
-    s = half_bits_to_float((keys ? c.k_scales : c.v_scales)[at]);
-    if (zeros) zp = zeros[at];
+    if (there && a == 0 && i == from && g < c.G) {
+      scales[(unit * c.G + g) * 16 + ts] = __builtin_bit_cast(uint16_t, s16);
+      if constexpr (AFF) zeros[(unit * c.G + g) * 16 + ts] = (uint8_t)zp;
+    }
   }
+
+  if (is_keys) {
+    if (there) {
+      uint32_t* const to = reinterpret_cast<uint32_t*>(packed + unit * (16 * DB) + ts * DB + a * 4 * C);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t u = (word >> (4 * e)) & 15u;
-    const int q = zeros ? (int)u - (int)zp : sx4(u);
-    if (d0 + e < c.D) store_row<DT>(out, o + e, (float)q * s);
+      for (int i = 0; i < C; ++i) to[i] = word[i];
+    }
+    return;
+  }
+  // --- values: bytes to [unit][channel pair][token]
+  __shared__ __attribute__((aligned(16))) uint8_t bytes[4 * DB * 16];
+  __shared__ int64_t units[4];
+  __shared__ uint32_t written[4];                    // a bit for each token of the unit
+  const uint64_t tokens = __ballot(there);           // lanes 4 t + a: a wavefront is a unit
+  if ((tid & (kWave - 1)) == 0) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) bits |= (uint32_t)((tokens >> (4 * t)) & 1) << t;
+    written[tid >> 6] = bits;
+  }
+  if (there) units[tid >> 6] = unit;                 // the same for all its tokens
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      bytes[(token >> 4) * (DB * 16) + (16 * i + 4 * a + k) * 16 + (token & 15)] = (uint8_t)(word[i] >> (8 * k));
+  __syncthreads();
+  for (int it = tid; it < 4 * DB; it += 256) {
+    const int u = it / DB, j = it % DB;
+    const uint32_t mask = written[u];
+    if (mask == 0) continue;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(&bytes[it * 16]);
+    uint8_t* const to = packed + units[u] * (16 * DB) + j * 16;
+    if (mask == 0xFFFFu) {
+      *reinterpret_cast<u32x4_t*>(to) = v;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+        if ((mask >> t) & 1u) to[t] = (uint8_t)(v[t / 4] >> (8 * (t % 4)));
+    }
   }
 }
 
-template <int DT, int LP, int LANES>
-void write_form(const CacheView& c, const RowsView& r, const RowArray& k, const RowArray& v, hipStream_t stream) {
-  const dim3 grid((unsigned)((r.rows + 256 / LP - 1) / (256 / LP)), (unsigned)c.heads, 2);
-  if (c.k_zeros) hipLaunchKernelGGL((cache_write_kernel<DT, LP, LANES, true>), grid, dim3(256), 0, stream, c, r, k, v);
-  else hipLaunchKernelGGL((cache_write_kernel<DT, LP, LANES, false>), grid, dim3(256), 0, stream, c, r, k, v);
+// ---------------------------------------------------------------- read
+
+template <int DT, int C, bool AFF>
+__global__ __launch_bounds__(256) void cache_read_kernel(CacheView c, RowsView r, RowArray keys, RowArray values) {
+  constexpr int DB = 16 * C;
+  StoreBlock w;
+  if (!find_store_block(r, blockIdx.x, &w)) return;
+  const int head = blockIdx.y, tid = threadIdx.x;
+  if (blockIdx.z == 0) {
+    const int token = tid >> 2, a = tid & 3;
+    const int64_t pos = w.base + token, at_row = pos - w.p0;
+    if (at_row < 0 || at_row >= w.rows) return;
+    const int64_t page = find_page(r, c, w.b, pos);
+    const int slot = (int)(pos & (((int64_t)1 << c.page_shift) - 1)), ts = slot & 15;
+    const int64_t unit = page < 0 ? 0 : c.unit(page, head, slot);
+    const uint32_t* const from = reinterpret_cast<const uint32_t*>(c.k_packed + unit * (16 * DB) + ts * DB + a * 4 * C);
+    Bits<DT>* const to = static_cast<Bits<DT>*>(keys.p) + (w.first + at_row) * keys.row_stride + head * keys.head_stride;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int d = 32 * i + 8 * a;
+      if (d >= c.D) break;
+      const uint32_t word = from[i];
+      const int64_t at = (unit * c.G + d / c.group) * 16 + ts;
+      const float s = half_bits_to_float(c.k_scales[at]);
+      const int zp = AFF ? c.k_zeros[at] : 0;
+      Pack<Bits<DT>, 8> out;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = (word >> (4 * e)) & 15u;
+        out.v[e] = bits_of<DT>(page < 0 ? 0.0f : (float)(AFF ? (int)u - zp : sx4(u)) * s);
+      }
+      if (keys.wide) {
+        *reinterpret_cast<Pack<Bits<DT>, 8>*>(to + d) = out;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (d + e < c.D) to[d + e] = out.v[e];
+      }
+    }
+    return;
+  }
+  for (int it = tid; it < 4 * DB; it += 256) {
+    const int u = it / DB, j = it % DB, d = 2 * j;
+    const int64_t pos0 = w.base + 16 * u, row0 = pos0 - w.p0;
+    if (d >= c.D || row0 + 15 < 0 || row0 >= w.rows) continue;
+    const int64_t page = find_page(r, c, w.b, pos0);
+    const int slot = (int)(pos0 & (((int64_t)1 << c.page_shift) - 1));
+    const int64_t unit = page < 0 ? 0 : c.unit(page, head, slot);
+    const u32x4_t bytes = *reinterpret_cast<const u32x4_t*>(c.v_packed + unit * (16 * DB) + j * 16);
+    const int64_t at = (unit * c.G + d / c.group) * 16;
+    const u32x4_t s0 = *reinterpret_cast<const u32x4_t*>(c.v_scales + at);
+    const u32x4_t s1 = *reinterpret_cast<const u32x4_t*>(c.v_scales + at + 8);
+    u32x4_t z = {0, 0, 0, 0};
+    if constexpr (AFF) z = *reinterpret_cast<const u32x4_t*>(c.v_zeros + at);
+    Bits<DT>* const to = static_cast<Bits<DT>*>(values.p) + (w.first + row0) * values.row_stride + head * values.head_stride + d;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const uint32_t b = (bytes[t / 4] >> (8 * (t % 4))) & 0xFFu;
+      const float s = half_bits_to_float((uint16_t)((t < 8 ? s0[t / 2] : s1[t / 2 - 4]) >> (16 * (t % 2))));
+      const int zp = AFF ? (z[t / 4] >> (8 * (t % 4))) & 0xFFu : 0;
+      const int q0 = AFF ? (int)(b & 15u) - zp : sx4(b & 15u), q1 = AFF ? (int)(b >> 4) - zp : sx4(b >> 4);
+      const Pack<Bits<DT>, 2> out = {bits_of<DT>(page < 0 ? 0.0f : (float)q0 * s),
+                                     bits_of<DT>(page < 0 ? 0.0f : (float)q1 * s)};
+      if (row0 + t < 0 || row0 + t >= w.rows) continue;
+      if (values.wide) {
+        *reinterpret_cast<Pack<Bits<DT>, 2>*>(to + t * values.row_stride) = out;
+      } else {
+        to[t * values.row_stride] = out.v[0];
+        if (d + 1 < c.D) to[t * values.row_stride + 1] = out.v[1];
+      }
+    }
+  }
 }
 
-template <int DT, int LP>
-void write_group(const CacheView& c, const RowsView& r, const RowArray& k, const RowArray& v, hipStream_t stream) {
-  // one group: the butterfly runs over all lanes of the row
-  const int lanes = c.G == 1 ? LP : c.group / 8;
-  if (lanes == 4) write_form<DT, LP, 4>(c, r, k, v, stream);
-  else if (lanes == 8) write_form<DT, LP, 8>(c, r, k, v, stream);
-  else if constexpr (LP >= 16) {
-    if (lanes == 16) write_form<DT, LP, 16>(c, r, k, v, stream);
-    else write_form<DT, LP, LP>(c, r, k, v, stream);
+// ---------------------------------------------------------------- launches
+
+dim3 store_grid(const CacheView& c, const RowsView& r) {
+  const int64_t units = r.starts ? r.rows / 64 + 2 * (int64_t)r.batch : r.batch;
+  return dim3((unsigned)units, (unsigned)c.heads, 2);
+}
+
+template <int DT, int C>
+void launch_store(bool write, const CacheView& c, const RowsView& r, const RowArray& k, const RowArray& v,
+                  hipStream_t stream) {
+  const dim3 grid = store_grid(c, r), block(256);
+  if (write) {
+    if (c.k_zeros) hipLaunchKernelGGL((cache_write_kernel<DT, C, true>), grid, block, 0, stream, c, r, k, v);
+    else hipLaunchKernelGGL((cache_write_kernel<DT, C, false>), grid, block, 0, stream, c, r, k, v);
+  } else {
+    if (c.k_zeros) hipLaunchKernelGGL((cache_read_kernel<DT, C, true>), grid, block, 0, stream, c, r, k, v);
+    else hipLaunchKernelGGL((cache_read_kernel<DT, C, false>), grid, block, 0, stream, c, r, k, v);
   }
 }
 
 template <int DT>
-void write_width(const CacheView& c, const RowsView& r, const RowArray& k, const RowArray& v, hipStream_t stream) {
-  if (c.C == 2) write_group<DT, 8>(c, r, k, v, stream);
-  else if (c.C <= 4) write_group<DT, 16>(c, r, k, v, stream);
-  else write_group<DT, 32>(c, r, k, v, stream);
+void launch_width(bool write, const CacheView& c, const RowsView& r, const RowArray& k, const RowArray& v,
+                  hipStream_t stream) {
+  switch (c.C) {
+    case 2: return launch_store<DT, 2>(write, c, r, k, v, stream);
+    case 3: return launch_store<DT, 3>(write, c, r, k, v, stream);
+    case 4: return launch_store<DT, 4>(write, c, r, k, v, stream);
+    case 6: return launch_store<DT, 6>(write, c, r, k, v, stream);
+    default: return launch_store<DT, 8>(write, c, r, k, v, stream);
+  }
 }
 
-template <int DT>
-void read_width(const CacheView& c, const RowsView& r, void* k, void* v, hipStream_t stream) {
-  const int LP = c.C == 2 ? 8 : c.C <= 4 ? 16 : 32;
-  const dim3 grid((unsigned)((r.rows + 256 / LP - 1) / (256 / LP)), (unsigned)c.heads, 2);
-  if (LP == 8) hipLaunchKernelGGL((cache_read_kernel<DT, 8>), grid, dim3(256), 0, stream, c, r, k, v);
-  else if (LP == 16) hipLaunchKernelGGL((cache_read_kernel<DT, 16>), grid, dim3(256), 0, stream, c, r, k, v);
-  else hipLaunchKernelGGL((cache_read_kernel<DT, 32>), grid, dim3(256), 0, stream, c, r, k, v);
+hipError_t launch_type(bool write, const CacheView& c, const RowsView& r, RowArray k, RowArray v, int dtype,
+                       hipStream_t stream) {
+  const int per16 = dtype == INT4DQ_ROWS_F32 ? 4 : 8;          // elements of 16 bytes
+  for (RowArray* x : {&k, &v})
+    x->wide = c.D % 8 == 0 && (uintptr_t)x->p % 16 == 0 && x->row_stride % per16 == 0 && x->head_stride % per16 == 0;
+  if (dtype == INT4DQ_ROWS_F32) launch_width<INT4DQ_ROWS_F32>(write, c, r, k, v, stream);
+  else if (dtype == INT4DQ_ROWS_F16) launch_width<INT4DQ_ROWS_F16>(write, c, r, k, v, stream);
+  else launch_width<INT4DQ_ROWS_BF16>(write, c, r, k, v, stream);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -186,18 +373,13 @@ void read_width(const CacheView& c, const RowsView& r, void* k, void* v, hipStre
 hipError_t launch_cache_write(const CacheView& c, const RowsView& r, const void* k, int64_t k_row_stride,
                               int64_t k_head_stride, const void* v, int64_t v_row_stride, int64_t v_head_stride,
                               int dtype, hipStream_t stream) {
-  const RowArray ka{k, k_row_stride, k_head_stride}, va{v, v_row_stride, v_head_stride};
-  if (dtype == INT4DQ_ROWS_F32) write_width<INT4DQ_ROWS_F32>(c, r, ka, va, stream);
-  else if (dtype == INT4DQ_ROWS_F16) write_width<INT4DQ_ROWS_F16>(c, r, ka, va, stream);
-  else write_width<INT4DQ_ROWS_BF16>(c, r, ka, va, stream);
-  return hipGetLastError();
+  return launch_type(true, c, r, RowArray{const_cast<void*>(k), k_row_stride, k_head_stride, 0},
+                     RowArray{const_cast<void*>(v), v_row_stride, v_head_stride, 0}, dtype, stream);
 }
 
 hipError_t launch_cache_read(const CacheView& c, const RowsView& r, void* k, void* v, int dtype, hipStream_t stream) {
-  if (dtype == INT4DQ_ROWS_F32) read_width<INT4DQ_ROWS_F32>(c, r, k, v, stream);
-  else if (dtype == INT4DQ_ROWS_F16) read_width<INT4DQ_ROWS_F16>(c, r, k, v, stream);
-  else read_width<INT4DQ_ROWS_BF16>(c, r, k, v, stream);
-  return hipGetLastError();
+  const int64_t row = (int64_t)c.heads * c.D;
+  return launch_type(false, c, r, RowArray{k, row, c.D, 0}, RowArray{v, row, c.D, 0}, dtype, stream);
 }
 
 }  // namespace int4dq

@@ -42,8 +42,8 @@
  *   - a position below 0, at or above max_pages * page_size, or on a page
  *     outside 0 .. pages-1 is not written, reads back as zeros, and takes no
  *     part in attention.
- * starts must not decrease. Two rows of one write call that come to lie on
- * the same slot (a page listed twice) leave either's codes there.
+ * starts must not decrease. Where two rows of one write call come to lie on the
+ * same slot (a page listed twice), what that slot holds afterwards is a mixture.
  */
 #ifndef INT4DQ_CACHE_H
 #define INT4DQ_CACHE_H
