@@ -28,6 +28,7 @@ struct CacheView {
   int64_t pages;
   int page_shift;   // log2 of the tokens on a page
   int heads, D, group, G, C;
+  int affine;       // whether there are zero points (known also where the pointers are not given)
 
   // Index of the 16-token unit that holds `slot` of `page`, counted over the
   // whole cache: its codes start at unit * 16 * DB bytes (keys and values) and

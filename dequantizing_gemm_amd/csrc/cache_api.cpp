@@ -69,7 +69,7 @@ int check(const char* fn, const int4_cache_t* c, const int4_cache_rows_t* r, boo
   const int D = (int)c->head_dim;
   const int group = c->group < D ? (int)c->group : D;
   *cv = CacheView{c->k_packed, c->k_scales, c->k_zeros, c->v_packed, c->v_scales, c->v_zeros, c->pages, shift,
-                  (int)c->heads, D, group, (D + group - 1) / group, int4dq::cache_blocks(D)};
+                  (int)c->heads, D, group, (D + group - 1) / group, int4dq::cache_blocks(D), c->k_zeros ? 1 : 0};
   *rv = RowsView{r->page_table, r->table_stride, r->max_pages, r->lengths, r->starts, (int)r->batch, r->rows};
   return INT4DQ_OK;
 }

@@ -10,9 +10,10 @@ namespace {
 
 // out = sum_i exp2(m_i - M) o_i / sum_i exp2(m_i - M) l_i over the chunks of a
 // tile that was shared out, for each of its rows. One block for each slot and head
-// (those whose slot is no tile's first leave at once) and, in y, a few of the
-// tile's rows; a channel quadruple a thread, the chunks dealt to 256 / (8 C) groups
-// of threads and joined through LDS.
+// (those whose slot is no tile's first leave at once) and, in y, a share of the
+// tile's rows; a channel quadruple a thread, 256 / (8 C) groups of threads. Up to 8
+// chunks: each group has a row of its own. More: the groups share out the chunks
+// of one row and are joined through LDS.
 template <int C>
 __global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
   constexpr int T = 8 * C, GROUPS = 256 / T;
@@ -28,7 +29,35 @@ __global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs
   const float* const base = ws.part + ((int64_t)slot * a.c.heads + kh) * size;
   const int lane = threadIdx.x & (kWave - 1), group = threadIdx.x / T, d = threadIdx.x % T * 4;
   __shared__ __attribute__((aligned(16))) float4_t sums[GROUPS][T];
-  for (int row = blockIdx.y; row < sched.tile_rows && tile.flat0 + row < tile.flats; row += gridDim.y) {
+  const int rows = tile.flats - tile.flat0 < sched.tile_rows ? tile.flats - tile.flat0 : sched.tile_rows;
+  const uint32_t ratio = a.ratio;
+  if (tile.chunks <= 8) {
+    for (int row = blockIdx.y * GROUPS + group; row < rows && group < GROUPS; row += gridDim.y * GROUPS) {
+      const float* const ml = base + (int64_t)sched.tile_rows * 32 * C + 2 * row;
+      float m[8], top = -1e30f, sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m[i] = ml[(i < tile.chunks ? i : 0) * next];
+        top = __builtin_fmaxf(top, m[i]);
+      }
+      float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < tile.chunks) {
+          const float f = __builtin_amdgcn_exp2f(m[i] - top);
+          sum += ml[i * next + 1] * f;
+          v += *reinterpret_cast<const float4_t*>(base + i * next + row * (32 * C) + d) * f;
+        }
+      v *= sum == 0.0f ? 0.0f : 1.0f / sum;
+      const uint32_t flat = tile.flat0 + row;
+      const int64_t at = (int64_t)(tile.first + flat / ratio) * a.c.heads * ratio + kh * ratio + flat % ratio;
+      const float o[4] = {v.x, v.y, v.z, v.w};
+      store_output<4>(a, at, d, o);
+      if (d == 0 && a.lse) a.lse[at] = lse_of(top, sum);
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const float* const ml = base + (int64_t)sched.tile_rows * 32 * C + 2 * row;
     float top = -1e30f;
     for (int i = lane; i < tile.chunks; i += kWave) top = __builtin_fmaxf(top, ml[i * next]);
@@ -48,16 +77,18 @@ __global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs
       sums[group][threadIdx.x % T] = v;
     }
     __syncthreads();
-    const uint32_t flat = tile.flat0 + row, ratio = a.ratio;
+    const uint32_t flat = tile.flat0 + row;
     const int64_t at = (int64_t)(tile.first + flat / ratio) * a.c.heads * ratio + kh * ratio + flat % ratio;
     if (threadIdx.x < T) {
       v = sums[0][threadIdx.x];
 #pragma unroll
       for (int i = 1; i < GROUPS; ++i) v += sums[i][threadIdx.x];
-      store_output(a, at, d, v * (sum == 0.0f ? 0.0f : 1.0f / sum));
+      v *= sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float o[4] = {v.x, v.y, v.z, v.w};
+      store_output<4>(a, at, d, o);
     }
     if (threadIdx.x == 0 && a.lse)
-      a.lse[at] = sum == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (top + __builtin_amdgcn_logf(sum));
+      a.lse[at] = lse_of(top, sum);
     __syncthreads();                                 // the sums are read
   }
 }

@@ -47,6 +47,8 @@
 
 namespace int4dq {
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
 // ---------------------------------------------------------------- wavefront sums
 
 // Inclusive sums over the lanes: within rows of 16 by shifts, then across rows.
@@ -234,308 +236,258 @@ __device__ __forceinline__ float query_value(const Words<4>& r, int e, int bf16)
   return bf16 ? __builtin_bit_cast(float, h << 16) : half_bits_to_float((uint16_t)h);
 }
 
-__device__ __forceinline__ uint16_t output_bits(float v, int bf16) {
-  if (!bf16) return __builtin_bit_cast(uint16_t, (_Float16)v);
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);   // NaN stays NaN
-  return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+// Two outputs as binary16 or bfloat16 patterns, rounded to nearest even.
+__device__ __forceinline__ uint32_t output_pair(float x, float y, int bf16) {
+  if (bf16) {
+    const bf16x2_t v = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+  const half2_t v = {(_Float16)x, (_Float16)y};
+  return __builtin_bit_cast(uint32_t, v);
 }
 
-// Channels d0 .. d0+3 of one output row (those below D).
-__device__ __forceinline__ void store_output(const AttentionArgs& a, int64_t row, int d0, float4_t v) {
+// Channels d0 .. d0 + N - 1 of one output row (N 4 or 8), those below D.
+template <int N>
+__device__ __forceinline__ void store_output(const AttentionArgs& a, int64_t row, int d0, const float* v) {
   uint16_t* const p = static_cast<uint16_t*>(a.out) + row * a.c.D + d0;
-  const uint16_t h[4] = {output_bits(v.x, a.bf16), output_bits(v.y, a.bf16), output_bits(v.z, a.bf16),
-                         output_bits(v.w, a.bf16)};
-  if (a.c.D % 4 == 0 && ((uintptr_t)a.out & 7) == 0) {
-    if (d0 < a.c.D)
-      *reinterpret_cast<u32x2_t*>(p) = u32x2_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+  Words<N / 2> w;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w.w[i] = output_pair(v[2 * i], v[2 * i + 1], a.bf16);
+  if (a.c.D % 8 == 0 && ((uintptr_t)a.out & 15) == 0) {
+    if (d0 >= a.c.D) return;
+    if constexpr (N == 4) *reinterpret_cast<u32x2_t*>(p) = u32x2_t{w.w[0], w.w[1]};
+    else *reinterpret_cast<u32x4_t*>(p) = u32x4_t{w.w[0], w.w[1], w.w[2], w.w[3]};
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (d0 + i < a.c.D) p[i] = h[i];
+    for (int i = 0; i < N; ++i)
+      if (d0 + i < a.c.D) p[i] = (uint16_t)(w.w[i / 2] >> (16 * (i & 1)));
   }
 }
 
-// ---------------------------------------------------------------- the kernel
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  return sum == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (m + __builtin_amdgcn_logf(sum));
+}
 
-// C blocks of 32 channels, GC of them to a scale (scale_blocks), QT tiles of 16
-// query rows.
-template <int C, int GC, int QT, bool AFF>
-__global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
-  constexpr int NG = C / GC, DB = 16 * C, TR = 16 * QT;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
-  const int row = lane & 15, quarter = lane >> 4;
-  const int heads = a.c.heads, kh = blockIdx.x % heads;
-  BlockWork work;
-  if (sched.target > 0 && blockIdx.x == gridDim.x - 1 && wave == 0) {
-    const int used = slots_used(a, sched);
-    if (lane == 0) *ws.used = used;
-  }
-  if (!find_block(a, sched, blockIdx.x / heads, &work)) return;
-  const int flat0 = work.tile * TR, flats = work.w.rows * a.ratio;
-  if (work.chunks > 1 && kh == 0 && threadIdx.x == 0)
-    ws.record[work.slot] = PartRecord{work.w.first, flat0, flats, work.chunk, work.chunks, {}};
+// ---------------------------------------------------------------- where a step's codes lie
 
-  // --- the tile's visible keys
-  const uint32_t ratio = (uint32_t)a.ratio;
-  int lo_first, hi_first, lo_last, hi_last;
-  visible(a, work.w, (uint32_t)flat0 / ratio, &lo_first, &hi_first);
-  visible(a, work.w, ((flat0 + TR < flats ? flat0 + TR : flats) - 1) / ratio, &lo_last, &hi_last);
-  int begin, end;
-  chunk_steps(lo_first, hi_last, work.chunk, work.chunks, &begin, &end);
+// The 16-token units of the cache that hold the four of a step (0 where there is
+// no page; bit u of `found` tells).
+struct Units {
+  int at[4];
+  uint32_t found;
+};
+struct Pages {
+  int p[4];
+};
 
-  // --- queries: loads only; a row that the tile does not have reads the last one
-  Words<4> raw[QT][C];
-  int lo[QT], hi[QT];
-  int64_t q_at[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int flat = flat0 + 16 * t + row;
-    const uint32_t f = flat < flats ? flat : flats - 1, token = f / ratio;
-    visible(a, work.w, token, &lo[t], &hi[t]);
-    if (flat >= flats) lo[t] = hi[t] = 0;
-    q_at[t] = (int64_t)(work.w.first + token) * a.q_row_stride + (int64_t)(kh * ratio + f % ratio) * a.q_head_stride;
-  }
-  if (a.q_wide) {
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int d = 32 * i + 8 * quarter;
-        raw[t][i] = load_words<4>(reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(a.q) + q_at[t] +
-                                                                   (d < a.c.D ? d : 0)));
-      }
-  } else {
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int d = 32 * i + 8 * quarter + 2 * e, last = a.c.D - 1;
-          const uint16_t* const p = static_cast<const uint16_t*>(a.q) + q_at[t];
-          raw[t][i].w[e] = p[d < last ? d : last] | (uint32_t)p[d + 1 < last ? d + 1 : last] << 16;
-        }
-  }
+// Page numbers come through scalar loads, ahead of their use: as vector loads they
+// would make the wait for them a wait for every load before them.
+struct PageTable {
+  typedef const int32_t __attribute__((address_space(4))) * ScalarPtr;
+  ScalarPtr table;
+  int shift, last, slots, page_units, head_unit, pages;
 
-  // --- loads of a step: the lane's key rows lie in the 16-token unit row / 4 of
-  // the step, its values and scales in unit `quarter`
-  typedef const int32_t __attribute__((address_space(4))) * ScalarPtr;         // read by scalar loads
-  const ScalarPtr table = (ScalarPtr)(uintptr_t)(a.r.table + (int64_t)work.b * a.r.table_stride);
-  const int key_off = ((row & 3) == 1 ? 2 : (row & 3) == 2 ? 1 : (row & 3)) * DB + quarter * 4 * C;
-  int group_of[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const int x = NG == 1 ? 0 : g * GC * 32 / a.c.group;
-    group_of[g] = x < a.c.G ? x : a.c.G - 1;
-  }
-  // The 16-token units of the cache that hold the four of a step (0 where there is
-  // no page; bit u of `found` tells). Page numbers come through scalar loads, two
-  // steps ahead: as vector loads they would make the wait for them a wait for
-  // every load before them.
-  struct Units {
-    int at[4];
-    uint32_t found;
-  };
-  struct Pages {
-    int p[4];
-  };
-  const int page_units = heads << (a.c.page_shift - 4), head_unit = kh << (a.c.page_shift - 4);
-  const int last_index = (int)a.r.max_pages - 1, slots = (1 << a.c.page_shift) - 1;
-  auto pages_of = [&](int step) {
+  __device__ __forceinline__ PageTable(const AttentionArgs& a, int b, int kh)
+      : table((ScalarPtr)(uintptr_t)(a.r.table + (int64_t)b * a.r.table_stride)), shift(a.c.page_shift),
+        last((int)a.r.max_pages - 1), slots((1 << a.c.page_shift) - 1), page_units(a.c.heads << (a.c.page_shift - 4)),
+        head_unit(kh << (a.c.page_shift - 4)), pages((int)a.c.pages) {}
+
+  __device__ __forceinline__ Pages pages_of(int step) const {
     Pages r;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int index = (step * kStep + 16 * u) >> a.c.page_shift;
-      r.p[u] = table[index < last_index ? index : last_index];
+      const int index = (step * kStep + 16 * u) >> shift;
+      r.p[u] = table[index < last ? index : last];
     }
     return r;
-  };
-  auto units_of = [&](int step, const Pages& pages) {
+  }
+  __device__ __forceinline__ Units units_of(int step, const Pages& x) const {
     Units r;
     r.found = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const bool ok = (uint32_t)pages.p[u] < (uint32_t)a.c.pages;
-      r.at[u] = ok ? pages.p[u] * page_units + head_unit + (((step * kStep + 16 * u) & slots) >> 4) : 0;
+      const bool ok = (uint32_t)x.p[u] < (uint32_t)pages;
+      r.at[u] = ok ? x.p[u] * page_units + head_unit + (((step * kStep + 16 * u) & slots) >> 4) : 0;
       r.found |= ok ? 1u << u : 0u;
     }
     return r;
-  };
-  auto pick = [&](const Units& x, int u) {
-    const int a0 = x.at[0], a1 = x.at[1], a2 = x.at[2], a3 = x.at[3];      // values: no address is selected
-    const int low = u & 1 ? a1 : a0, high = u & 1 ? a3 : a2;
-    return u & 2 ? high : low;
-  };
-  Words<C> kw[4];
-  Words<4> vw[C];
-  uint16_t ksc[NG], vsc[NG];             // of token `row` of the quarter's unit
-  uint8_t kz[AFF ? NG : 1];
-  Words<4> vz[AFF ? NG : 1];             // of the unit's 16 tokens
-  auto load_keys = [&](const Units& x) {
-    const int ku = pick(x, row >> 2), vu = pick(x, quarter);
-    const uint8_t* const p = a.c.k_packed + (int64_t)ku * (16 * DB) + key_off;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) kw[n] = load_words<C>(p + n * 4 * DB);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int64_t at = ((int64_t)vu * a.c.G + group_of[g]) * 16;
-      ksc[g] = a.c.k_scales[at + row];
-      if constexpr (AFF) kz[g] = a.c.k_zeros[at + row];
-    }
-  };
-  auto load_values = [&](const Units& x) {
-    const int vu = pick(x, quarter);
-    const uint8_t* const p = a.c.v_packed + (int64_t)vu * (16 * DB) + row * 16;
-#pragma unroll
-    for (int j = 0; j < C; ++j) vw[j] = load_words<4>(p + j * 256);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int64_t at = ((int64_t)vu * a.c.G + group_of[g]) * 16;
-      vsc[g] = a.c.v_scales[at + row];
-      if constexpr (AFF) vz[g] = load_words<4>(a.c.v_zeros + at);
-    }
-  };
-
-  int step = begin + wave;
-  Units units{};
-  Pages pages{};
-  if (step < end) {
-    units = units_of(step, pages_of(step));
-    pages = pages_of(step + 4);
-    load_keys(units);
-    load_values(units);
   }
+};
 
-  // --- queries: operand, factor of the scores, sums for affine codes
+__device__ __forceinline__ int pick(const Units& x, int u) {
+  const int a0 = x.at[0], a1 = x.at[1], a2 = x.at[2], a3 = x.at[3];      // values: no address is selected
+  const int low = u & 1 ? a1 : a0, high = u & 1 ? a3 : a2;
+  return u & 2 ? high : low;
+}
+
+// Token of its unit, within 4, whose key row a lane of `row` takes.
+__device__ __forceinline__ int key_token(int row) { return (row & 3) == 1 ? 2 : (row & 3) == 2 ? 1 : (row & 3); }
+
+// Scales and zero points of a step as a lane holds them: of token `row` of the
+// unit `quarter`, and for the values' zero points of all its tokens.
+template <int NG, bool AFF>
+struct StepScales {
+  uint16_t k[NG], v[NG];
+  uint8_t kz[AFF ? NG : 1];
+  Words<4> vz[AFF ? NG : 1];
+};
+
+// ---------------------------------------------------------------- a wavefront's rows
+
+// 16 QT query rows of one key/value head: lane (row, quarter) holds query row `row`
+// of each tile of 16, and of a step the scores of the tokens of unit `quarter`.
+template <int C, int GC, int QT, bool AFF>
+struct Rows {
+  static constexpr int NG = C / GC;
+  int row, quarter;
+  int flat0, flats;                      // the first flat row, and the sequence's number of them
+  int lo[QT], hi[QT];                    // visible keys
   half8_t q[QT][C];
   float factor[QT], qsum[QT][AFF ? NG : 1];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // channels from head_dim on, and rows that the tile does not have, are 0
-        const int have = flat0 + 16 * t + row < flats ? a.c.D - 32 * i - 8 * quarter - 2 * e : 0;
-        raw[t][i].w[e] &= have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u;
-        top = __builtin_fmaxf(top, __builtin_fabsf(query_value(raw[t][i], 2 * e, a.bf16)));
-        top = __builtin_fmaxf(top, __builtin_fabsf(query_value(raw[t][i], 2 * e + 1, a.bf16)));
-      }
-    top = rows_max(top);
-    // top * 2^up in [2^13, 2^14)
-    const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
-    const int up = top > 0.0f ? (e > 110 ? -97 : 13 - e) : 0;
-    factor[t] = __builtin_ldexpf(a.scale * 1.44269504088896340736f, -up);
-#pragma unroll
-    for (int g = 0; g < (AFF ? NG : 1); ++g) qsum[t][g] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      _Float16 h[8];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        h[n] = (_Float16)__builtin_ldexpf(query_value(raw[t][i], n, a.bf16), up);
-        if constexpr (AFF) qsum[t][i / GC] += (float)h[n];
-      }
-      q[t][i] = half8_t{h[0], h[4], h[1], h[5], h[2], h[6], h[3], h[7]};
-    }
-#pragma unroll
-    for (int g = 0; g < (AFF ? NG : 0); ++g) qsum[t][g] = rows_sum(qsum[t][g]);
-  }
-
   float4_t acc[QT][2 * C];               // [.][2 j]: channels of the low nibbles of byte rows 16 j .., [2 j + 1]: high
   float m[QT], l[QT], zsum[QT][AFF ? NG : 1];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    m[t] = -1e30f;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int g = 0; g < (AFF ? NG : 1); ++g) zsum[t][g] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2 * C; ++j) acc[t][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  }
+  float s[QT][16];                       // scores, then probabilities: tokens token_of(0) .. token_of(15)
+  int group_of[NG];
 
-  for (; step < end; step += 4) {
-    const int next = step + 4;
-    const uint32_t found = units.found;
-    units = units_of(next, pages);
-    pages = pages_of(next + 4);
-
-    // --- scores
-    float s[QT][16], ks[NG], zk[AFF ? NG : 1];
+  // Query loads only; a row that the tile does not have reads the sequence's last.
+  __device__ __forceinline__ void load(const AttentionArgs& a, const SequenceWork& w, int kh, Words<4> raw[QT][C]) {
+    const uint32_t ratio = (uint32_t)a.ratio;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      ks[g] = half_bits_to_float(ksc[g]);
-      if constexpr (AFF) zk[g] = 8.0f - (float)kz[g];
+      const int x = NG == 1 ? 0 : g * GC * 32 / a.c.group;
+      group_of[g] = x < a.c.G ? x : a.c.G - 1;
     }
-    each<4>([&](auto nn) {
-      constexpr int n = decltype(nn)::value;
-      half8_t k[C];
+    const uint16_t* at[QT];
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        half2_t c[4];
-        code_pairs<AFF>(kw[n].w[i], c);
-        k[i] = as_half8(c);
-      }
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float4_t dot = {0.0f, 0.0f, 0.0f, 0.0f};
-          if constexpr (AFF)               // (8 - z) sum q
-            each<4>([&](auto ii) {
-              constexpr int i = decltype(ii)::value;
-              dot[i] = qsum[t][g] * of_token<token_of(4 * n + i)>(zk[g]);
-            });
-#pragma unroll
-          for (int i = g * GC; i < (g + 1) * GC; ++i)
-            dot = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i], q[t][i], dot, 0, 0, 0);
-          each<4>([&](auto ii) {
-            constexpr int i = decltype(ii)::value, tok = token_of(4 * n + i);
-            const float x = dot[i] * of_token<tok>(ks[g]);
-            s[t][4 * n + i] = g == 0 ? x : s[t][4 * n + i] + x;
-          });
-        }
-      }
-      // no instruction, but an order: this tile's scores are finished before the
-      // next one's codes are taken apart, which keeps the live registers few
+    for (int t = 0; t < QT; ++t) {
+      const int flat = flat0 + 16 * t + row;
+      const uint32_t f = flat < flats ? flat : flats - 1, token = f / ratio;
+      visible(a, w, token, &lo[t], &hi[t]);
+      if (flat >= flats) lo[t] = hi[t] = 0;
+      at[t] = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + token) * a.q_row_stride +
+              (int64_t)(kh * ratio + f % ratio) * a.q_head_stride;
+    }
+    if (a.q_wide) {
 #pragma unroll
       for (int t = 0; t < QT; ++t)
-        asm volatile("" : "+v"(s[t][4 * n]), "+v"(s[t][4 * n + 1]), "+v"(s[t][4 * n + 2]), "+v"(s[t][4 * n + 3]));
-      if constexpr (n < 3) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) asm volatile("" : "+v"(kw[n + 1].w[i]));
-      }
-    });
-    if (next < end) load_keys(units);
-
-    // --- masks: only where a row does not see the whole step
-    const int token0 = step * kStep + 16 * quarter;
-    const bool masked = step * kStep < lo_last || (step + 1) * kStep > hi_first || found != 15u;
-    if (masked) {
-      const bool there = (found >> quarter) & 1u;
+        for (int i = 0; i < C; ++i) {
+          const int d = 32 * i + 8 * quarter;
+          raw[t][i] = load_words<4>(reinterpret_cast<const uint8_t*>(at[t] + (d < a.c.D ? d : 0)));
+        }
+    } else {
 #pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        const int from = lo[t] - token0, to = there ? hi[t] - token0 : -1;
+      for (int t = 0; t < QT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (token_of(i) < from || token_of(i) >= to) s[t][i] = -__builtin_inff();
-      }
-      // scales of tokens that the sequence does not have (their memory may hold
-      // anything) take no part in the largest scale
-      const int have = there ? work.w.keys - token0 : 0;
+        for (int i = 0; i < C; ++i)
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-        if (row >= have) vsc[g] = 0;
+          for (int e = 0; e < 4; ++e) {
+            const int d = 32 * i + 8 * quarter + 2 * e, last = a.c.D - 1;
+            raw[t][i].w[e] = at[t][d < last ? d : last] | (uint32_t)at[t][d + 1 < last ? d + 1 : last] << 16;
+          }
     }
+  }
 
-    // --- the running reference: largest score plus the exponent of the largest
-    // scale, an upper bound of log2 of every weight
-    uint32_t big = vsc[0];
+  // The operand, the factor of the scores and the sums for affine codes.
+  __device__ __forceinline__ void start(const AttentionArgs& a, Words<4> raw[QT][C]) {
 #pragma unroll
-    for (int g = 1; g < NG; ++g) big = vsc[g] > big ? vsc[g] : big;
+    for (int t = 0; t < QT; ++t) {
+      // the largest magnitude: its pattern orders like an unsigned number
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // channels from head_dim on, and rows that the tile does not have, are 0
+          const int have = flat0 + 16 * t + row < flats ? a.c.D - 32 * i - 8 * quarter - 2 * e : 0;
+          const uint32_t x = raw[t][i].w[e] & (have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u);
+          raw[t][i].w[e] = x;
+          const uint32_t low = x & 0x7FFFu, high = (x >> 16) & 0x7FFFu;
+          top = low > top ? low : top;
+          top = high > top ? high : top;
+        }
+      const Words<4> one = {{top, 0, 0, 0}};
+      const float most = rows_max(query_value(one, 0, a.bf16));
+      // most * 2^up in [2^13, 2^14)
+      const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;
+      const int up = most > 0.0f ? (e > 110 ? -97 : 13 - e) : 0;
+      factor[t] = __builtin_ldexpf(a.scale * 1.44269504088896340736f, -up);
+#pragma unroll
+      for (int g = 0; g < (AFF ? NG : 1); ++g) qsum[t][g] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        _Float16 h[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          h[n] = (_Float16)__builtin_ldexpf(query_value(raw[t][i], n, a.bf16), up);
+          if constexpr (AFF) qsum[t][i / GC] += (float)h[n];
+        }
+        q[t][i] = half8_t{h[0], h[4], h[1], h[5], h[2], h[6], h[3], h[7]};
+      }
+#pragma unroll
+      for (int g = 0; g < (AFF ? NG : 0); ++g) qsum[t][g] = rows_sum(qsum[t][g]);
+      m[t] = -1e30f;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < (AFF ? NG : 1); ++g) zsum[t][g] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2 * C; ++j) acc[t][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
+
+  // Scores of key tile n from its operand (a block of 32 channels each).
+  template <int n>
+  __device__ __forceinline__ void score(const half8_t k[C], const StepScales<NG, AFF>& x) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const float ks = half_bits_to_float(x.k[g]);
+        float4_t dot = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (AFF) {               // (8 - z) sum q
+          const float z = 8.0f - (float)x.kz[g];
+          each<4>([&](auto ii) {
+            constexpr int i = decltype(ii)::value;
+            dot[i] = qsum[t][g] * of_token<token_of(4 * n + i)>(z);
+          });
+        }
+#pragma unroll
+        for (int i = g * GC; i < (g + 1) * GC; ++i)
+          dot = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i], q[t][i], dot, 0, 0, 0);
+        each<4>([&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          const float y = dot[i] * of_token<token_of(4 * n + i)>(ks);
+          s[t][4 * n + i] = g == 0 ? y : s[t][4 * n + i] + y;
+        });
+      }
+    }
+  }
+
+  // Hides the step's tokens that a row does not see. Scales of tokens that the
+  // sequence does not have (their memory may hold anything) become 0.
+  __device__ __forceinline__ void hide(int step, uint32_t found, int keys, StepScales<NG, AFF>& x) {
+    const int token0 = step * kStep + 16 * quarter;
+    const bool there = (found >> quarter) & 1u;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const int from = lo[t] - token0, to = there ? hi[t] - token0 : -1;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (token_of(i) < from || token_of(i) >= to) s[t][i] = -__builtin_inff();
+    }
+    const int have = there ? keys - token0 : 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      if (row >= have) x.v[g] = 0;
+  }
+
+  // Moves the running reference where it has to and turns the scores into
+  // probabilities. The reference is the largest score plus the exponent of the
+  // largest scale: an upper bound of log2 of every weight, less 9.
+  __device__ __forceinline__ void settle(const StepScales<NG, AFF>& x) {
+    uint32_t big = x.v[0];
+#pragma unroll
+    for (int g = 1; g < NG; ++g) big = x.v[g] > big ? x.v[g] : big;
     const float spread = (float)((int)(row_umax(big) >> 10) - 14 - 9);
     bool move = false;
     float cand[QT];
@@ -560,8 +512,6 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
         for (int j = 0; j < 2 * C; ++j) acc[t][j] *= shrink;
       }
     }
-
-    // --- probabilities
 #pragma unroll
     for (int t = 0; t < QT; ++t)
 #pragma unroll
@@ -569,98 +519,268 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
         s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], factor[t], -m[t]));
         l[t] += s[t][i];
       }
+  }
 
-    // --- values, a group of channels at a time
+  // The weights of group g, probability times scale in binary16, as the operand of
+  // the product with the values: tokens 0 .. 7 of the unit, then 8 .. 15.
+  __device__ __forceinline__ void weights(int g, bool masked, const StepScales<NG, AFF>& x, half8_t w[QT][2]) {
+    const float vs = half_bits_to_float(x.v[g]);
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      half2_t pair[8];
+      if (!masked) {
+        each<8>([&](auto ii) {
+          constexpr int i = 2 * decltype(ii)::value;
+          pair[i / 2] = half2_t{(_Float16)(s[t][i] * of_token<token_of(i)>(vs)),
+                                (_Float16)(s[t][i + 1] * of_token<token_of(i + 1)>(vs))};
+        });
+      } else {                             // a hidden token's scale may be infinite or NaN
+        each<8>([&](auto ii) {
+          constexpr int i = 2 * decltype(ii)::value;
+          const float y0 = s[t][i] * of_token<token_of(i)>(vs), y1 = s[t][i + 1] * of_token<token_of(i + 1)>(vs);
+          pair[i / 2] = half2_t{(_Float16)(s[t][i] == 0.0f ? 0.0f : y0), (_Float16)(s[t][i + 1] == 0.0f ? 0.0f : y1)};
+        });
+      }
+      if constexpr (AFF) {
+        const half2_t off = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {      // 1024 + z, then z - 8
+          const uint32_t zw = x.vz[g].w[i / 2];
+          const uint32_t z = ((i & 1 ? zw >> 8 : zw) & 0x00FF00FFu) | 0x64006400u;
+          zsum[t][g] = __builtin_amdgcn_fdot2(pair[i], __builtin_bit_cast(half2_t, z) + off, zsum[t][g], false);
+        }
+      }
+      w[t][0] = as_half8(pair);
+      w[t][1] = as_half8(pair + 4);
+    }
+  }
+
+  // Adds the products of byte rows 16 j .. of the values, tokens 8 u .. of each unit.
+  __device__ __forceinline__ void add(int j, half8_t even, half8_t odd, const half8_t w[QT][2], int u) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      acc[t][2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(even, w[t][u], acc[t][2 * j], 0, 0, 0);
+      acc[t][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(odd, w[t][u], acc[t][2 * j + 1], 0, 0, 0);
+    }
+  }
+
+  // The lane's sums over its row's four lanes; then result() gives the channels
+  // 32 j + 8 quarter .. + 7 of its row.
+  __device__ __forceinline__ void finish(int t) {
+    l[t] = rows_sum(l[t]);
+#pragma unroll
+    for (int g = 0; g < (AFF ? NG : 0); ++g) zsum[t][g] = rows_sum(zsum[t][g]);
+  }
+  __device__ __forceinline__ void result(int t, int j, float factor_, float v[8]) const {
+    const float z = AFF ? zsum[t][AFF ? j / GC : 0] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = (acc[t][2 * j][i] - z) * factor_;
+      v[2 * i + 1] = (acc[t][2 * j + 1][i] - z) * factor_;
+    }
+  }
+};
+
+// Value operands of two words (two channels of eight tokens) each.
+template <bool AFF>
+__device__ __forceinline__ void value_operands(uint32_t w0, uint32_t w1, half8_t* even, half8_t* odd) {
+  half2_t c[8];
+  code_pairs<AFF>(w0, c);
+  code_pairs<AFF>(w1, c + 4);
+  const half2_t lows[4] = {c[0], c[2], c[4], c[6]}, highs[4] = {c[1], c[3], c[5], c[7]};
+  *even = as_half8(lows);
+  *odd = as_half8(highs);
+}
+
+template <int C, bool AFF>
+__device__ __forceinline__ void key_operands(const Words<C>& w, half8_t k[C]) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    half2_t c[4];
+    code_pairs<AFF>(w.w[i], c);
+    k[i] = as_half8(c);
+  }
+}
+
+template <int NG, bool AFF>
+__device__ __forceinline__ void load_key_scales(const CacheView& c, int unit, int row, const int group_of[NG],
+                                                StepScales<NG, AFF>* x) {
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int64_t at = ((int64_t)unit * c.G + group_of[g]) * 16;
+    x->k[g] = c.k_scales[at + row];
+    if constexpr (AFF) x->kz[g] = c.k_zeros[at + row];
+  }
+}
+template <int NG, bool AFF>
+__device__ __forceinline__ void load_value_scales(const CacheView& c, int unit, int row, const int group_of[NG],
+                                                  StepScales<NG, AFF>* x) {
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int64_t at = ((int64_t)unit * c.G + group_of[g]) * 16;
+    x->v[g] = c.v_scales[at + row];
+    if constexpr (AFF) x->vz[g] = load_words<4>(c.v_zeros + at);
+  }
+}
+
+// What a block does first: its share, the record of a partial result, the number
+// of them. False if it has no share.
+__device__ __forceinline__ bool begin_block(const AttentionArgs& a, const Schedule& sched, const Workspace& ws,
+                                            BlockWork* work) {
+  const int heads = a.c.heads;
+  if (sched.target > 0 && blockIdx.x == gridDim.x - 1 && threadIdx.x < kWave) {
+    const int used = slots_used(a, sched);
+    if (threadIdx.x == 0) *ws.used = used;
+  }
+  if (!find_block(a, sched, blockIdx.x / heads, work)) return false;
+  if (work->chunks > 1 && blockIdx.x % heads == 0 && threadIdx.x == 0)
+    ws.record[work->slot] = PartRecord{work->w.first, work->tile * sched.tile_rows, work->w.rows * a.ratio, work->chunk,
+                                       work->chunks, {}};
+  return true;
+}
+
+// Visible keys of flat rows [flat0, flat0 + n) that the sequence has: of the first
+// row and of the last.
+struct Span {
+  int lo_first, hi_first, lo_last, hi_last;
+  __device__ __forceinline__ Span(const AttentionArgs& a, const SequenceWork& w, int flat0, int n) {
+    const int flats = w.rows * a.ratio;
+    visible(a, w, (uint32_t)flat0 / (uint32_t)a.ratio, &lo_first, &hi_first);
+    visible(a, w, (uint32_t)((flat0 + n < flats ? flat0 + n : flats) - 1) / (uint32_t)a.ratio, &lo_last, &hi_last);
+  }
+  // Whether some row does not see some token of the step.
+  __device__ __forceinline__ bool masks(int step) const {
+    return step * kStep < lo_last || (step + 1) * kStep > hi_first;
+  }
+};
+
+// ---------------------------------------------------------------- few rows
+
+// C blocks of 32 channels, GC of them to a scale (scale_blocks), QT tiles of 16
+// query rows. The block's four wavefronts take turns on the steps; their results
+// are joined through LDS.
+template <int C, int GC, int QT, bool AFF>
+__global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
+  constexpr int NG = C / GC, DB = 16 * C, TR = 16 * QT;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
+  const int heads = a.c.heads, kh = blockIdx.x % heads;
+  BlockWork work;
+  if (!begin_block(a, sched, ws, &work)) return;
+  Rows<C, GC, QT, AFF> r;
+  r.row = lane & 15;
+  r.quarter = lane >> 4;
+  r.flat0 = work.tile * TR;
+  r.flats = work.w.rows * a.ratio;
+  const Span span(a, work.w, r.flat0, TR);
+  int begin, end;
+  chunk_steps(span.lo_first, span.hi_last, work.chunk, work.chunks, &begin, &end);
+  Words<4> raw[QT][C];
+  r.load(a, work.w, kh, raw);
+
+  // A lane's key rows lie in the 16-token unit row / 4 of the step, its values and
+  // scales in unit `quarter`.
+  const PageTable table(a, work.b, kh);
+  const int key_off = key_token(r.row) * DB + r.quarter * 4 * C;
+  Words<C> kw[4];
+  Words<4> vw[C];
+  StepScales<NG, AFF> sc;
+  auto load_keys = [&](const Units& x) {
+    const uint8_t* const p = a.c.k_packed + (int64_t)pick(x, r.row >> 2) * (16 * DB) + key_off;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) kw[n] = load_words<C>(p + n * 4 * DB);
+    load_key_scales(a.c, pick(x, r.quarter), r.row, r.group_of, &sc);
+  };
+  auto load_values = [&](const Units& x) {
+    const int vu = pick(x, r.quarter);
+    const uint8_t* const p = a.c.v_packed + (int64_t)vu * (16 * DB) + r.row * 16;
+#pragma unroll
+    for (int j = 0; j < C; ++j) vw[j] = load_words<4>(p + j * 256);
+    load_value_scales(a.c, vu, r.row, r.group_of, &sc);
+  };
+  int step = begin + wave;
+  Units units{};
+  Pages pages{};
+  if (step < end) {
+    units = table.units_of(step, table.pages_of(step));
+    pages = table.pages_of(step + 4);
+    load_keys(units);
+    load_values(units);
+  }
+  r.start(a, raw);
+
+  for (; step < end; step += 4) {
+    const int next = step + 4;
+    const uint32_t found = units.found;
+    units = table.units_of(next, pages);
+    pages = table.pages_of(next + 4);
+    each<4>([&](auto nn) {
+      constexpr int n = decltype(nn)::value;
+      half8_t k[C];
+      key_operands<C, AFF>(kw[n], k);
+      r.template score<n>(k, sc);
+      // no instruction, but an order: this tile's scores are finished before the
+      // next one's codes are taken apart, which keeps the live registers few
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+        asm volatile("" : "+v"(r.s[t][4 * n]), "+v"(r.s[t][4 * n + 1]), "+v"(r.s[t][4 * n + 2]), "+v"(r.s[t][4 * n + 3]));
+      if constexpr (n < 3) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) asm volatile("" : "+v"(kw[n + 1].w[i]));
+      }
+    });
+    if (next < end) load_keys(units);
+    const bool masked = span.masks(step) || found != 15u;
+    if (masked) r.hide(step, found, work.w.keys, sc);
+    r.settle(sc);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       half8_t w[QT][2];
-      const float vs = half_bits_to_float(vsc[g]);
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        half2_t pair[8];
-        if (!masked) {
-          each<8>([&](auto ii) {
-            constexpr int i = 2 * decltype(ii)::value;
-            pair[i / 2] = half2_t{(_Float16)(s[t][i] * of_token<token_of(i)>(vs)),
-                                  (_Float16)(s[t][i + 1] * of_token<token_of(i + 1)>(vs))};
-          });
-        } else {                         // a hidden token's scale may be infinite or NaN
-          each<8>([&](auto ii) {
-            constexpr int i = 2 * decltype(ii)::value;
-            const float x = s[t][i] * of_token<token_of(i)>(vs), y = s[t][i + 1] * of_token<token_of(i + 1)>(vs);
-            pair[i / 2] = half2_t{(_Float16)(s[t][i] == 0.0f ? 0.0f : x), (_Float16)(s[t][i + 1] == 0.0f ? 0.0f : y)};
-          });
-        }
-        if constexpr (AFF) {
-          const half2_t off = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {     // 1024 + z, then z - 8
-            const uint32_t z = ((i & 1 ? vz[g].w[i / 2] >> 8 : vz[g].w[i / 2]) & 0x00FF00FFu) | 0x64006400u;
-            zsum[t][g] = __builtin_amdgcn_fdot2(pair[i], __builtin_bit_cast(half2_t, z) + off, zsum[t][g], false);
-          }
-        }
-        w[t][0] = as_half8(pair);
-        w[t][1] = as_half8(pair + 4);
-      }
+      r.weights(g, masked, sc, w);
 #pragma unroll
       for (int j = g * GC; j < (g + 1) * GC; ++j) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          // a word: two channels of four tokens
-          half2_t c[8];
-          code_pairs<AFF>(vw[j].w[2 * u], c);
-          code_pairs<AFF>(vw[j].w[2 * u + 1], c + 4);
-          const half2_t lows[4] = {c[0], c[2], c[4], c[6]}, highs[4] = {c[1], c[3], c[5], c[7]};
-          const half8_t even = as_half8(lows), odd = as_half8(highs);
-#pragma unroll
-          for (int t = 0; t < QT; ++t) {
-            acc[t][2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(even, w[t][u], acc[t][2 * j], 0, 0, 0);
-            acc[t][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(odd, w[t][u], acc[t][2 * j + 1], 0, 0, 0);
-          }
+          half8_t even, odd;
+          value_operands<AFF>(vw[j].w[2 * u], vw[j].w[2 * u + 1], &even, &odd);
+          r.add(j, even, odd, w, u);
         }
         if (j + 1 < C) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(vw[j + 1].w[i]) : "v"(acc[QT - 1][2 * j + 1]));
+          for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(vw[j + 1].w[i]) : "v"(r.acc[QT - 1][2 * j + 1]));
         }
       }
     }
     if (next < end) load_values(units);
   }
 
-  // --- join the block's wavefronts, 16 rows at a time. Lane (row, quarter) holds
-  // channels 32 j + 8 quarter .. + 7 of query row `row`.
+  // --- join the wavefronts, 16 rows at a time
   __shared__ float ml[2][4][16];
   __shared__ __attribute__((aligned(16))) float rows_out[4][16][32 * C + 4];
   const int tid = threadIdx.x, orow = tid >> 4;
+  const uint32_t ratio = (uint32_t)a.ratio;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    const float lt = rows_sum(l[t]);
-    float zt[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) zt[g] = AFF ? rows_sum(zsum[t][AFF ? g : 0]) : 0.0f;
-    if (quarter == 0) {
-      ml[0][wave][row] = m[t];
-      ml[1][wave][row] = lt;
+    r.finish(t);
+    if (r.quarter == 0) {
+      ml[0][wave][r.row] = r.m[t];
+      ml[1][wave][r.row] = r.l[t];
     }
     __syncthreads();
-    const float top = __builtin_fmaxf(__builtin_fmaxf(ml[0][0][row], ml[0][1][row]),
-                                      __builtin_fmaxf(ml[0][2][row], ml[0][3][row]));
-    const float shrink = __builtin_amdgcn_exp2f(m[t] - top);
+    const float top = __builtin_fmaxf(__builtin_fmaxf(ml[0][0][r.row], ml[0][1][r.row]),
+                                      __builtin_fmaxf(ml[0][2][r.row], ml[0][3][r.row]));
+    const float shrink = __builtin_amdgcn_exp2f(r.m[t] - top);
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       float v[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = (acc[t][2 * j][i] - zt[j / GC]) * shrink;
-        v[2 * i + 1] = (acc[t][2 * j + 1][i] - zt[j / GC]) * shrink;
-      }
-      float4_t* const to = reinterpret_cast<float4_t*>(&rows_out[wave][row][32 * j + 8 * quarter]);
+      r.result(t, j, shrink, v);
+      float4_t* const to = reinterpret_cast<float4_t*>(&rows_out[wave][r.row][32 * j + 8 * r.quarter]);
       to[0] = float4_t{v[0], v[1], v[2], v[3]};
       to[1] = float4_t{v[4], v[5], v[6], v[7]};
     }
     __syncthreads();
-    const int flat = flat0 + 16 * t + orow;
-    if (flat < flats) {
+    const int flat = r.flat0 + 16 * t + orow;
+    if (flat < r.flats) {
       float mm = ml[0][0][orow];
 #pragma unroll
       for (int i = 1; i < 4; ++i) mm = __builtin_fmaxf(mm, ml[0][i][orow]);
@@ -669,15 +789,15 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
       for (int i = 0; i < 4; ++i) sum += ml[1][i][orow] * __builtin_amdgcn_exp2f(ml[0][i][orow] - mm);
       const bool whole = work.chunks == 1;
       const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-      const int64_t orow_at = (work.w.first + (uint32_t)flat / ratio) * ((int64_t)heads * ratio) + kh * ratio +
-                              (uint32_t)flat % ratio;
+      const int64_t at = (int64_t)(work.w.first + (uint32_t)flat / ratio) * heads * ratio + kh * ratio + (uint32_t)flat % ratio;
       float* const slot = ws.part + ((int64_t)work.slot * heads + kh) * partial_floats(TR, C);
       for (int d = (tid & 15) * 4; d < 32 * C; d += 64) {
         float4_t v = *reinterpret_cast<const float4_t*>(&rows_out[0][orow][d]);
 #pragma unroll
         for (int i = 1; i < 4; ++i) v += *reinterpret_cast<const float4_t*>(&rows_out[i][orow][d]);
         v *= inv;
-        if (whole) store_output(a, orow_at, d, v);
+        const float o[4] = {v.x, v.y, v.z, v.w};
+        if (whole) store_output<4>(a, at, d, o);
         else *reinterpret_cast<float4_t*>(slot + (16 * t + orow) * (32 * C) + d) = v;
       }
       if ((tid & 15) == 0) {
@@ -685,11 +805,200 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
           slot[TR * 32 * C + 2 * (16 * t + orow)] = mm;
           slot[TR * 32 * C + 2 * (16 * t + orow) + 1] = sum;
         } else if (a.lse) {
-          a.lse[orow_at] = sum == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (mm + __builtin_amdgcn_logf(sum));
+          a.lse[at] = lse_of(mm, sum);
         }
       }
     }
     __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+
+// The form for prompts: each of the block's wavefronts has 16 QT rows of its own
+// (128 in all: four wavefronts of 32 rows, or eight of 16 where the registers do
+// not hold more) and all take the same steps. The codes of a step are taken apart
+// once a block: each wavefront turns its share of them into operands and leaves
+// those in LDS, in the lanes' order, for all, one step ahead of their use (two
+// buffers, one barrier a step).
+template <int C, int GC, int QT, bool AFF>
+__global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
+  constexpr int NG = C / GC, DB = 16 * C, TR = kWideRows;
+  constexpr int VJ = (C + 3) / 4;        // byte rows (of 16) of the values that a wavefront prepares
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
+  const int heads = a.c.heads, kh = blockIdx.x % heads;
+  BlockWork work;
+  if (!begin_block(a, sched, ws, &work)) return;
+  Rows<C, GC, QT, AFF> r;
+  r.row = lane & 15;
+  r.quarter = lane >> 4;
+  r.flat0 = work.tile * TR + wave * 16 * QT;
+  r.flats = work.w.rows * a.ratio;
+  const bool rows_here = r.flat0 < r.flats;
+  const Span all(a, work.w, work.tile * TR, TR);
+  const Span span(a, work.w, rows_here ? r.flat0 : work.tile * TR, 16 * QT);
+  int begin, end;
+  chunk_steps(all.lo_first, all.hi_last, work.chunk, work.chunks, &begin, &end);
+  // the steps of which this wavefront's rows see something
+  const int first = span.lo_first / kStep, last = rows_here && span.hi_last > span.lo_first ? (span.hi_last - 1) / kStep : -1;
+  Words<4> raw[QT][C];
+  r.load(a, work.w, kh, raw);
+
+  const PageTable table(a, work.b, kh);
+  // The shares: one key tile and one in four of the values' byte rows for each of
+  // four wavefronts, or either for each of eight.
+  const bool does_keys = QT == 2 || wave < 4, does_values = QT == 2 || wave >= 4;
+  const int share = wave & 3;
+  const int key_off = key_token(r.row) * DB + share * 4 * DB + r.quarter * 4 * C;
+  __shared__ __attribute__((aligned(16))) u32x4_t keys[2][4 * C][kWave];            // [4 tiles][C]
+  __shared__ __attribute__((aligned(16))) u32x4_t values[2][4 * C][kWave];          // [C][2 halves][even, odd]
+  Words<C> kw;
+  Words<4> vw[VJ];
+  StepScales<NG, AFF> sc, sc_next;
+  auto load = [&](const Units& x) {
+    const int vu = pick(x, r.quarter);
+    if (does_keys) kw = load_words<C>(a.c.k_packed + (int64_t)pick(x, r.row >> 2) * (16 * DB) + key_off);
+    if (does_values) {
+      const uint8_t* const p = a.c.v_packed + (int64_t)vu * (16 * DB) + r.row * 16;
+#pragma unroll
+      for (int i = 0; i < VJ; ++i) {
+        const int j = share + 4 * i;
+        vw[i] = load_words<4>(p + (j < C ? j : C - 1) * 256);
+      }
+    }
+    load_key_scales(a.c, vu, r.row, r.group_of, &sc_next);
+    load_value_scales(a.c, vu, r.row, r.group_of, &sc_next);
+  };
+  auto prepare = [&](int buffer) {
+    if (does_keys) {
+      half8_t k[C];
+      key_operands<C, AFF>(kw, k);
+#pragma unroll
+      for (int i = 0; i < C; ++i) keys[buffer][share * C + i][lane] = __builtin_bit_cast(u32x4_t, k[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VJ; ++i) {
+      const int j = share + 4 * i;
+      if (does_values && j < C) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          half8_t even, odd;
+          value_operands<AFF>(vw[i].w[2 * u], vw[i].w[2 * u + 1], &even, &odd);
+          values[buffer][4 * j + 2 * u][lane] = __builtin_bit_cast(u32x4_t, even);
+          values[buffer][4 * j + 2 * u + 1][lane] = __builtin_bit_cast(u32x4_t, odd);
+        }
+      }
+    }
+  };
+
+  int step = begin;
+  Units units{};
+  Pages pages{};
+  uint32_t found = 0, found_next = 0;
+  if (step < end) {
+    units = table.units_of(step, table.pages_of(step));
+    pages = table.pages_of(step + 1);
+    found = units.found;
+    load(units);
+  }
+  r.start(a, raw);
+  if (step < end) {
+    prepare(0);
+    sc = sc_next;
+    if (step + 1 < end) {
+      units = table.units_of(step + 1, pages);
+      pages = table.pages_of(step + 2);
+      found_next = units.found;
+      load(units);
+    }
+    lds_barrier();
+  }
+#pragma unroll 1
+  for (int buffer = 0; step < end; ++step, buffer ^= 1) {
+    if (step >= first && step <= last) {
+      // Operands are read from LDS one tile of keys, or one byte row of values, ahead
+      // of the products that take them; the empty statements keep that order.
+      half8_t k[2][C], v[2][4];
+      auto read_keys = [&](int n, half8_t* to) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) to[i] = __builtin_bit_cast(half8_t, keys[buffer][n * C + i][lane]);
+        asm volatile("" ::: "memory");
+      };
+      auto read_values = [&](int j, half8_t* to) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = __builtin_bit_cast(half8_t, values[buffer][4 * j + i][lane]);
+        asm volatile("" ::: "memory");
+      };
+      read_keys(0, k[0]);
+      each<4>([&](auto nn) {
+        constexpr int n = decltype(nn)::value;
+        if constexpr (n < 3) read_keys(n + 1, k[(n + 1) & 1]);
+        r.template score<n>(k[n & 1], sc);
+      });
+      read_values(0, v[0]);
+      const bool masked = span.masks(step) || found != 15u;
+      if (masked) r.hide(step, found, work.w.keys, sc);
+      r.settle(sc);
+      each<NG>([&](auto gg) {
+        constexpr int g = decltype(gg)::value;
+        half8_t w[QT][2];
+        r.weights(g, masked, sc, w);
+        each<GC>([&](auto jj) {
+          constexpr int j = g * GC + decltype(jj)::value;
+          if constexpr (j + 1 < C) read_values(j + 1, v[(j + 1) & 1]);
+          r.add(j, v[j & 1][0], v[j & 1][1], w, 0);
+          r.add(j, v[j & 1][2], v[j & 1][3], w, 1);
+        });
+      });
+    }
+    if (step + 1 < end) {
+      prepare(buffer ^ 1);               // last read in the step before, which all have left
+      sc = sc_next;
+      found = found_next;
+      if (step + 2 < end) {
+        units = table.units_of(step + 2, pages);
+        pages = table.pages_of(step + 3);
+        found_next = units.found;
+        load(units);
+      }
+      lds_barrier();
+    }
+  }
+
+  if (!rows_here) return;
+  const uint32_t ratio = (uint32_t)a.ratio;
+  const bool whole = work.chunks == 1;
+  float* const slot = ws.part + ((int64_t)work.slot * heads + kh) * partial_floats(TR, C);
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    r.finish(t);
+    const int flat = r.flat0 + 16 * t + r.row;
+    if (flat >= r.flats) continue;
+    const int64_t at = (int64_t)(work.w.first + (uint32_t)flat / ratio) * heads * ratio + kh * ratio + (uint32_t)flat % ratio;
+    const float inv = whole ? (r.l[t] == 0.0f ? 0.0f : 1.0f / r.l[t]) : 1.0f;
+    const int in_tile = wave * 16 * QT + 16 * t + r.row;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      float v[8];
+      r.result(t, j, inv, v);
+      const int d = 32 * j + 8 * r.quarter;
+      if (whole) {
+        store_output<8>(a, at, d, v);
+      } else {
+        float4_t* const to = reinterpret_cast<float4_t*>(slot + (int64_t)in_tile * (32 * C) + d);
+        to[0] = float4_t{v[0], v[1], v[2], v[3]};
+        to[1] = float4_t{v[4], v[5], v[6], v[7]};
+      }
+    }
+    if (r.quarter == 0) {
+      if (!whole) {
+        slot[TR * 32 * C + 2 * in_tile] = r.m[t];
+        slot[TR * 32 * C + 2 * in_tile + 1] = r.l[t];
+      } else if (a.lse) {
+        a.lse[at] = lse_of(r.m[t], r.l[t]);
+      }
+    }
   }
 }
 

@@ -21,8 +21,10 @@ namespace int4dq {
 
 constexpr int kStep = 64;                // tokens of a wavefront's step
 
+constexpr int kWideRows = 128;           // rows of a tile in the form for prompts
+
 struct Schedule {
-  int tile_rows;
+  int tile_rows;                         // kWideRows: that form
   int target;                            // 0: every tile in one block
   int min_steps;
   int units;                             // blocks per key/value head
@@ -100,10 +102,19 @@ inline int scale_blocks(const CacheView& c) {
   return c.C % blocks == 0 ? blocks : 1;
 }
 
-// The tallest tile (in 16 rows) whose accumulators, scores and operands stay in
-// registers: wide heads and many groups take more of them a row.
-constexpr int max_tiles(int C, int groups) {
-  return groups * C <= 8 ? 2 : 1;
+// Tiles of 16 rows a wavefront whose accumulators, scores and operands stay in
+// registers, in the form for few rows (at most) and in the one for prompts: wide
+// heads and many groups, affine ones above all, take more registers a row.
+constexpr int max_tiles(int C, int groups, bool affine) { return groups * C <= (affine ? 4 : 8) && C <= 4 ? 2 : 1; }
+constexpr int wide_tiles(int C, int groups, bool affine) {
+  return groups * C >= (affine ? 32 : 64) ? 0 : C <= 4 && !(affine && groups > 1) ? 2 : 1;      // 0: no such form
+}
+
+// Blocks of a form that a CU holds at once, by their registers and LDS.
+constexpr int resident_blocks(int C, int groups, bool affine, int tile_rows) {
+  if (tile_rows == kWideRows) return wide_tiles(C, groups, affine);              // of 4 wavefronts, or 1 of 8
+  if (tile_rows == 32) return C == 2 && !affine ? 3 : 2;
+  return C == 2 ? 4 : C == 3 ? 3 : C == 4 ? (affine && groups > 2 ? 2 : 3) : groups * C >= (affine ? 32 : 64) ? 1 : 2;
 }
 
 // The workspace: `slots` partial results for each head (the rows of a tile, then
@@ -138,20 +149,22 @@ __host__ __device__ inline Workspace workspace_at(void* p, const Schedule& s, in
 
 constexpr int kComputeUnits = 256;
 
-// Tiles of 16 rows for token generation, 32 where the sequences' rows fill them.
+// Tiles of 16 rows for token generation, of 32 where the sequences' rows fill
+// them, the form for prompts from more rows than one of its tiles holds (8 sequences
+// of 2650 tokens on average: 96 rows 39 us against its 48, 128 rows 43 against 51).
 inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   Schedule s{};
   const int64_t mean = (r.rows * ratio + r.batch - 1) / r.batch;
-  const int most = 16 * max_tiles(c.C, c.C / scale_blocks(c));
-  s.tile_rows = mean <= 16 ? 16 : 32;
-  if (s.tile_rows > most) s.tile_rows = most;
-  const int resident = s.tile_rows == 16 ? 3 : 2;      // blocks on a CU
+  const int groups = c.C / scale_blocks(c), most = 16 * max_tiles(c.C, groups, c.affine);
+  const bool wide = mean > kWideRows && wide_tiles(c.C, groups, c.affine) > 0;
+  s.tile_rows = wide ? kWideRows : mean <= 16 ? 16 : most;
+  const int resident = resident_blocks(c.C, groups, c.affine, s.tile_rows);
   s.target = (resident * kComputeUnits + c.heads - 1) / c.heads;
   s.share = 1.001f / (float)s.target;
-  s.min_steps = 4;
-  // Where the page table holds at most 1024 tokens a sequence, every tile is left
-  // to one block (4 steps a wavefront) and the join kernel's launch is saved.
-  if ((r.max_pages << c.page_shift) <= 16 * kStep) s.target = 0;
+  s.min_steps = 16;                      // four for each wavefront of the form for few rows
+  // Where no sequence can have more, every tile is left to one block and the join
+  // kernel's launch is saved.
+  if ((r.max_pages << c.page_shift) <= s.min_steps * kStep) s.target = 0;
   s.units = (int)(s.target + r.rows * ratio / s.tile_rows + r.batch);
   return s;
 }

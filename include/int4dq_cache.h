@@ -149,7 +149,7 @@ int int4_cache_attention(const int4_cache_t *cache, const int4_cache_rows_t *row
 /*
  * Workspace bytes of int4_cache_attention for these sizes (no pointer in the
  * descriptors is read or has to be set, except that starts = NULL says one row
- * a sequence); 0: the call does not use one. -1 on invalid sizes.
+ * a sequence and k_zeros = NULL symmetric codes); 0: the call does not use one. -1 on invalid sizes.
  */
 int64_t int4_cache_attention_workspace_bytes(const int4_cache_t *cache,
                                              const int4_cache_rows_t *rows, int64_t q_heads);

@@ -70,7 +70,7 @@ struct Arrays {
 static CacheView view(int D, int group, int heads, int shift, int pages) {
   if (group > D) group = D;
   return CacheView{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, pages, shift, heads, D, group,
-                   (D + group - 1) / group, cache_blocks(D)};
+                   (D + group - 1) / group, cache_blocks(D), (int)pick(0, 1)};
 }
 
 static void rows_and_pages() {
@@ -135,8 +135,9 @@ static void schedules() {
     a.causal = (int)pick(0, 1);
     a.window = a.causal && pick(0, 1) ? pick(1, 5000) : 0;
     Schedule s = plan_of(a.c, a.r, a.ratio);
-    CHECK(s.tile_rows == 16 || s.tile_rows == 32, "tile height");
-    CHECK(s.tile_rows <= 16 * max_tiles(a.c.C, a.c.C / scale_blocks(a.c)), "a tile height that has a form");
+    CHECK(s.tile_rows == 16 || s.tile_rows == 32 || s.tile_rows == kWideRows, "tile height");
+    CHECK(s.tile_rows != kWideRows || wide_tiles(a.c.C, a.c.C / scale_blocks(a.c), a.c.affine) > 0, "a form for prompts");
+    CHECK(s.tile_rows == kWideRows || s.tile_rows <= 16 * max_tiles(a.c.C, a.c.C / scale_blocks(a.c), a.c.affine), "a tile height that has a form");
     CHECK(a.c.C % scale_blocks(a.c) == 0 && (a.c.G == 1 || a.c.group % (32 * scale_blocks(a.c)) == 0), "blocks to a scale");
     if (trial % 5 == 4) { s.units -= s.target; s.target = 0; }
     {
@@ -194,7 +195,7 @@ static void schedules() {
 static void refusals() {
   alignas(256) static unsigned char arena[4096];
   int4_cache_t c{arena, (uint16_t*)arena, nullptr, arena, (uint16_t*)arena, nullptr, 4, 64, 2, 128, 64};
-  int4_cache_rows_t r{(int32_t*)arena, 5, 5, (int32_t*)arena, (int32_t*)arena, 3, 7};
+  int4_cache_rows_t r{(int32_t*)arena, 50, 50, (int32_t*)arena, (int32_t*)arena, 3, 7};
   void* const P = arena;
   auto all = [&](const char* needle) {
     const int before = calls;
