@@ -305,8 +305,10 @@ __device__ __forceinline__ int key_token(int row) { return (row & 3) == 1 ? 2 : 
 // unit `quarter`, and for the values' zero points of all its tokens.
 template <int NG, bool AFF>
 struct StepScales {
-  uint16_t k[NG], v[NG];
-  uint8_t kz[AFF ? NG : 1];
+  // 32-bit registers, as the loads leave them: a narrower type would be masked as
+  // soon as it arrives, and that be a wait for the load where it was issued.
+  uint32_t k[NG], v[NG];
+  uint32_t kz[AFF ? NG : 1];
   Words<4> vz[AFF ? NG : 1];
 };
 
@@ -420,7 +422,7 @@ struct Rows {
     for (int t = 0; t < QT; ++t) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const float ks = half_bits_to_float(x.k[g]);
+        const float ks = half_bits_to_float((uint16_t)x.k[g]);
         float4_t dot = {0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (AFF) {               // (8 - z) sum q
           const float z = 8.0f - (float)x.kz[g];
@@ -443,7 +445,7 @@ struct Rows {
 
   // Hides the step's tokens that a row does not see. Scales of tokens that the
   // sequence does not have (their memory may hold anything) become 0.
-  __device__ __forceinline__ void hide(int step, uint32_t found, int keys, StepScales<NG, AFF>& x) {
+  __device__ __forceinline__ void hide(int step, uint32_t found, int keys, uint32_t vs[NG]) {
     const int token0 = step * kStep + 16 * quarter;
     const bool there = (found >> quarter) & 1u;
 #pragma unroll
@@ -456,16 +458,16 @@ struct Rows {
     const int have = there ? keys - token0 : 0;
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-      if (row >= have) x.v[g] = 0;
+      if (row >= have) vs[g] = 0;
   }
 
   // Moves the running reference where it has to and turns the scores into
   // probabilities. The reference is the largest score plus the exponent of the
   // largest scale: an upper bound of log2 of every weight, less 9.
-  __device__ __forceinline__ void settle(const StepScales<NG, AFF>& x) {
-    uint32_t big = x.v[0];
+  __device__ __forceinline__ void settle(const uint32_t vs[NG]) {
+    uint32_t big = vs[0];
 #pragma unroll
-    for (int g = 1; g < NG; ++g) big = x.v[g] > big ? x.v[g] : big;
+    for (int g = 1; g < NG; ++g) big = vs[g] > big ? vs[g] : big;
     const float spread = (float)((int)(row_umax(big) >> 10) - 14 - 9);
     bool move = false;
     float cand[QT];
@@ -501,8 +503,8 @@ struct Rows {
 
   // The weights of group g, probability times scale in binary16, as the operand of
   // the product with the values: tokens 0 .. 7 of the unit, then 8 .. 15.
-  __device__ __forceinline__ void weights(int g, bool masked, const StepScales<NG, AFF>& x, half8_t w[QT][2]) {
-    const float vs = half_bits_to_float(x.v[g]);
+  __device__ __forceinline__ void weights(int g, bool masked, uint32_t scale, const StepScales<NG, AFF>& x, half8_t w[QT][2]) {
+    const float vs = half_bits_to_float((uint16_t)scale);
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       half2_t pair[8];
@@ -688,9 +690,12 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
   r.start(a, raw);
 
   for (; step < end; step += 4) {
-    const int next = step + 4;
+    // The loads for the next step are always issued, after the last one for this step
+    // again (out of the L2): behind a branch, every wait would have to assume the
+    // fewest loads in flight, and wait for the newest.
+    const int next = step + 4 < end ? step + 4 : step;
     const uint32_t found = units.found;
-    units = table.units_of(next, pages);
+    if (next > step) units = table.units_of(next, pages);
     pages = table.pages_of(next + 4);
     each<4>([&](auto nn) {
       constexpr int n = decltype(nn)::value;
@@ -707,14 +712,18 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
         for (int i = 0; i < C; ++i) asm volatile("" : "+v"(kw[n + 1].w[i]));
       }
     });
-    if (next < end) load_keys(units);
+    load_keys(units);
     const bool masked = span.masks(step) || found != 15u;
-    if (masked) r.hide(step, found, work.w.keys, sc);
-    r.settle(sc);
+    // a copy: changed in place, the scales would have to be moved where they arrive
+    uint32_t vs[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) vs[g] = sc.v[g];
+    if (masked) r.hide(step, found, work.w.keys, vs);
+    r.settle(vs);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       half8_t w[QT][2];
-      r.weights(g, masked, sc, w);
+      r.weights(g, masked, vs[g], sc, w);
 #pragma unroll
       for (int j = g * GC; j < (g + 1) * GC; ++j) {
 #pragma unroll
@@ -729,7 +738,7 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, S
         }
       }
     }
-    if (next < end) load_values(units);
+    load_values(units);
   }
 
   // --- join the wavefronts, 16 rows at a time
@@ -884,12 +893,10 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
   if (step < end) {
     prepare(0);
     sc = sc_next;
-    if (step + 1 < end) {
-      units = table.units_of(step + 1, pages);
-      pages = table.pages_of(step + 2);
-      found_next = units.found;
-      load(units);
-    }
+    if (step + 1 < end) units = table.units_of(step + 1, pages);
+    pages = table.pages_of(step + 2);
+    found_next = units.found;
+    load(units);
     lds_barrier();
   }
 #pragma unroll 1
@@ -916,12 +923,15 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
       });
       read_values(0, v[0]);
       const bool masked = span.masks(step) || found != 15u;
-      if (masked) r.hide(step, found, work.w.keys, sc);
-      r.settle(sc);
+      uint32_t vs[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) vs[g] = sc.v[g];
+      if (masked) r.hide(step, found, work.w.keys, vs);
+      r.settle(vs);
       each<NG>([&](auto gg) {
         constexpr int g = decltype(gg)::value;
         half8_t w[QT][2];
-        r.weights(g, masked, sc, w);
+        r.weights(g, masked, vs[g], sc, w);
         each<GC>([&](auto jj) {
           constexpr int j = g * GC + decltype(jj)::value;
           if constexpr (j + 1 < C) read_values(j + 1, v[(j + 1) & 1]);
@@ -930,18 +940,16 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
         });
       });
     }
-    if (step + 1 < end) {
-      prepare(buffer ^ 1);               // last read in the step before, which all have left
-      sc = sc_next;
-      found = found_next;
-      if (step + 2 < end) {
-        units = table.units_of(step + 2, pages);
-        pages = table.pages_of(step + 3);
-        found_next = units.found;
-        load(units);
-      }
-      lds_barrier();
-    }
+    // (at the end the last step's loads and operands once more, for no one: see the
+    // loads of the form for few rows)
+    prepare(buffer ^ 1);                 // last read in the step before, which all have left
+    sc = sc_next;
+    found = found_next;
+    if (step + 2 < end) units = table.units_of(step + 2, pages);
+    pages = table.pages_of(step + 3);
+    found_next = units.found;
+    load(units);
+    lds_barrier();
   }
 
   if (!rows_here) return;
