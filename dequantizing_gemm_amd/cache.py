@@ -256,9 +256,11 @@ def _workspace_bytes(cache, plan, q_heads):
 
 def cache_attention_workspace_bytes(cache: Int4Cache, batch: int, rows: int, q_heads: int) -> int:
     """Bytes of workspace int4_cache_attention uses for these sizes: ``rows`` rows
-    of ``q_heads`` query heads over ``batch`` sequences (0: none)."""
+    of ``q_heads`` query heads over ``batch`` sequences, whatever their page tables
+    (a call whose table is short takes less, or none)."""
     one = None if rows == batch else 1
-    return _workspace_bytes(cache, _RowsStruct(None, 0, 0, None, one, batch, rows), q_heads)
+    most = 2 ** 31 - 1
+    return _workspace_bytes(cache, _RowsStruct(None, most, most, None, one, batch, rows), q_heads)
 
 
 def cache_attention_workspace(cache: Int4Cache, batch: int, rows: int, q_heads: int) -> torch.Tensor:

@@ -8,6 +8,53 @@ namespace int4dq {
 
 namespace {
 
+// The blocks and slots of the sequences before each, for batches that a wavefront
+// does not look through at once: one block, a thread a sequence.
+__global__ __launch_bounds__(1024) void cache_attention_plan_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+  __shared__ float works[16];
+  __shared__ PlanEntry sums[2][16];
+  float all = 0.0f;
+  for (int b = tid; b < a.r.batch; b += 1024) {
+    const SequenceWork w = sequence_work(a, sched.tile_rows, b);
+    all += (float)w.tiles * (float)w.steps;
+  }
+  all = lane_scan(all);
+  if (lane == kWave - 1) works[wave] = all;
+  __syncthreads();
+  all = 0.0f;
+  for (int i = 0; i < 16; ++i) all += works[i];
+  const float each_step = blocks_per_step(sched, all);
+  int blocks = 0, slots = 0;
+  for (int b0 = 0, turn = 0; b0 < a.r.batch; b0 += 1024, turn ^= 1) {
+    const int b = b0 + tid;
+    int mine = 0, mine_slots = 0;
+    if (b < a.r.batch) {
+      const SequenceWork w = sequence_work(a, sched.tile_rows, b);
+      const int chunks = chunks_of(w.steps, each_step);
+      mine = chunks * w.tiles;
+      mine_slots = chunks > 1 ? mine : 0;
+    }
+    int upto = lane_scan(mine), slots_upto = lane_scan(mine_slots);
+    if (lane == kWave - 1) sums[turn][wave] = PlanEntry{upto, slots_upto};
+    __syncthreads();                     // two buffers: the one written next was read before this
+    upto += blocks;
+    slots_upto += slots;
+    for (int i = 0; i < 16; ++i) {
+      const PlanEntry x = sums[turn][i];
+      upto += i < wave ? x.blocks : 0;
+      slots_upto += i < wave ? x.slots : 0;
+      blocks += x.blocks;
+      slots += x.slots;
+    }
+    if (b < a.r.batch) ws.plan[b] = PlanEntry{upto - mine, slots_upto - mine_slots};
+  }
+  if (tid == 0) {
+    ws.plan[a.r.batch] = PlanEntry{blocks, slots};
+    *ws.used = slots;
+  }
+}
+
 // out = sum_i exp2(m_i - M) o_i / sum_i exp2(m_i - M) l_i over the chunks of a
 // tile that was shared out, for each of its rows. One block for each slot and head
 // (those whose slot is no tile's first leave at once) and, in y, a share of the
@@ -95,6 +142,7 @@ __global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs
 
 template <int C>
 hipError_t launch_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream) {
+  if (s.planned) hipLaunchKernelGGL(cache_attention_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s, ws);
   hipError_t e = launch_attention_width<C>(a, s, ws, stream);
   if (e != hipSuccess || s.target == 0) return e;
   const unsigned rows = (unsigned)(a.r.starts || a.ratio > 4 ? 4 : a.ratio);
@@ -113,14 +161,14 @@ extern template hipError_t launch_attention_width<8>(const AttentionArgs&, const
 
 int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int ratio) {
   const Schedule s = plan_of(c, r, ratio);
-  return s.target == 0 ? 0 : workspace_bytes(s, c.heads, c.C);
+  return s.target == 0 ? 0 : workspace_bytes(s, c.heads, c.C, r.batch);
 }
 
 hipError_t launch_cache_attention(const AttentionArgs& a, void* workspace, int64_t bytes, hipStream_t stream) {
   Schedule s = plan_of(a.c, a.r, a.ratio);
   if (bytes < cache_attention_workspace(a.c, a.r, a.ratio)) {
     s.units -= s.target;
-    s.target = 0;
+    s.target = s.planned = 0;
   }
   const Workspace ws = workspace_at(workspace, s, a.c.heads, a.c.C);
   switch (a.c.C) {

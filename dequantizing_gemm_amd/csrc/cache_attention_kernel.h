@@ -77,63 +77,56 @@ struct BlockWork {
   SequenceWork w;
 };
 
-// Slots of partial results that the call uses in all.
-__device__ __forceinline__ int slots_used(const AttentionArgs& a, const Schedule& s) {
-  const int lane = threadIdx.x & (kWave - 1);
-  float all = 0.0f;
-  for (int b = lane; b < a.r.batch; b += kWave) {
-    const SequenceWork x = sequence_work(a, s.tile_rows, b);
-    all += (float)x.tiles * (float)x.steps;
-  }
-  const float each_step = blocks_per_step(s, lane_value(lane_scan(all), kWave - 1));
-  int slots = 0;
-  for (int b = lane; b < a.r.batch; b += kWave) {
-    const SequenceWork x = sequence_work(a, s.tile_rows, b);
-    const int chunks = chunks_of(x.steps, each_step);
-    if (chunks > 1) slots += chunks * x.tiles;
-  }
-  return lane_value(lane_scan(slots), kWave - 1);
-}
-
 // The share of block `unit` of its head; every lane of the wavefront takes part.
-// False if it has none.
-__device__ __forceinline__ bool find_block(const AttentionArgs& a, const Schedule& s, int unit, BlockWork* out) {
+// False if it has none. `used`: the slots of partial results in all, where this
+// counts them (0 otherwise).
+__device__ __forceinline__ bool find_block(const AttentionArgs& a, const Schedule& s, const Workspace& ws, int unit,
+                                           BlockWork* out, int* used) {
   const int lane = threadIdx.x & (kWave - 1);
-  float all = 0.0f;
-  SequenceWork w{};
-  for (int b = lane; b < a.r.batch; b += kWave) {
-    const SequenceWork x = sequence_work(a, s.tile_rows, b);
-    all += (float)x.tiles * (float)x.steps;
-    if (b < kWave) w = x;
-  }
-  const float each_step = blocks_per_step(s, lane_value(lane_scan(all), kWave - 1));
-  int blocks = 0, slots = 0;
-  for (int b0 = 0; b0 < a.r.batch; b0 += kWave) {
-    const int b = b0 + lane;
-    int chunks = 0;
-    if (b < a.r.batch) {
-      if (b0 > 0) w = sequence_work(a, s.tile_rows, b);
-      chunks = chunks_of(w.steps, each_step);
-    }
-    const int mine = b < a.r.batch ? chunks * w.tiles : 0, mine_slots = chunks > 1 ? mine : 0;
-    const int upto = blocks + lane_scan(mine), slots_upto = slots + lane_scan(mine_slots);
+  int i;                                 // the block, counted from the sequence's first
+  *used = 0;
+  if (s.target > 0 && !s.planned) {      // all sequences at once
+    const SequenceWork w = lane < a.r.batch ? sequence_work(a, s.tile_rows, lane) : SequenceWork{};
+    const float all = lane_value(lane_scan((float)w.tiles * (float)w.steps), kWave - 1);
+    const int chunks = w.tiles > 0 ? chunks_of(w.steps, blocks_per_step(s, all)) : 0;
+    const int mine = chunks * w.tiles, mine_slots = chunks > 1 ? mine : 0;
+    const int upto = lane_scan(mine), slots_upto = lane_scan(mine_slots);
+    *used = lane_value(slots_upto, kWave - 1);
     const uint64_t hit = __ballot(unit >= upto - mine && unit < upto);
-    if (hit) {
-      const int at = __builtin_ctzll(hit);
-      out->b = b0 + at;
-      out->w = SequenceWork{lane_value(w.first, at), lane_value(w.end, at), lane_value(w.rows, at),
-                            lane_value(w.length, at), lane_value(w.keys, at), lane_value(w.tiles, at), 0};
-      out->chunks = lane_value(chunks, at);
-      const int i = unit - lane_value(upto - mine, at);
-      out->chunk = i % out->chunks;
-      out->tile = out->w.tiles - 1 - i / out->chunks;      // tiles that see most first
-      out->slot = lane_value(slots_upto - mine_slots, at) + i;
-      return true;
+    if (hit == 0) return false;
+    const int at = __builtin_ctzll(hit);
+    out->b = at;
+    out->w = SequenceWork{lane_value(w.first, at), lane_value(w.end, at), lane_value(w.rows, at),
+                          lane_value(w.length, at), lane_value(w.keys, at), lane_value(w.tiles, at), 0};
+    out->chunks = lane_value(chunks, at);
+    i = unit - lane_value(upto - mine, at);
+    out->slot = lane_value(slots_upto - mine_slots, at) + i;
+  } else if (s.target > 0) {
+    out->b = lane_search(a.r.batch, unit, [&](int b) { return (int64_t)ws.plan[b].blocks; });
+    const PlanEntry from = ws.plan[out->b], to = ws.plan[out->b + 1];
+    i = unit - from.blocks;
+    if (i < 0 || i >= to.blocks - from.blocks) return false;
+    out->w = sequence_work(a, s.tile_rows, out->b);
+    out->chunks = (to.blocks - from.blocks) / out->w.tiles;
+    out->slot = from.slots + i;
+  } else {
+    if (a.r.starts) {
+      out->b = lane_search(a.r.batch, unit, [&](int b) { return tiles_before(a, s, b); });
+      i = unit - (int)tiles_before(a, s, out->b);
+    } else {
+      const int tiles = (a.ratio + s.tile_rows - 1) / s.tile_rows;
+      out->b = unit / tiles;
+      if (out->b >= a.r.batch) return false;
+      i = unit % tiles;
     }
-    blocks = lane_value(upto, kWave - 1);
-    slots = lane_value(slots_upto, kWave - 1);
+    out->w = sequence_work(a, s.tile_rows, out->b);
+    if (i < 0 || i >= out->w.tiles) return false;
+    out->chunks = 1;
+    out->slot = 0;
   }
-  return false;
+  out->chunk = i % out->chunks;
+  out->tile = out->w.tiles - 1 - i / out->chunks;            // tiles that see most first
+  return true;
 }
 
 // ---------------------------------------------------------------- operands
@@ -608,11 +601,10 @@ __device__ __forceinline__ void load_value_scales(const CacheView& c, int unit, 
 __device__ __forceinline__ bool begin_block(const AttentionArgs& a, const Schedule& sched, const Workspace& ws,
                                             BlockWork* work) {
   const int heads = a.c.heads;
-  if (sched.target > 0 && blockIdx.x == gridDim.x - 1 && threadIdx.x < kWave) {
-    const int used = slots_used(a, sched);
-    if (threadIdx.x == 0) *ws.used = used;
-  }
-  if (!find_block(a, sched, blockIdx.x / heads, work)) return false;
+  int used;
+  const bool found = find_block(a, sched, ws, blockIdx.x / heads, work, &used);
+  if (sched.target > 0 && !sched.planned && blockIdx.x == 0 && threadIdx.x == 0) *ws.used = used;
+  if (!found) return false;
   if (work->chunks > 1 && blockIdx.x % heads == 0 && threadIdx.x == 0)
     ws.record[work->slot] = PartRecord{work->w.first, work->tile * sched.tile_rows, work->w.rows * a.ratio, work->chunk,
                                        work->chunks, {}};

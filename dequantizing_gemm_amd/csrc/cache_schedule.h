@@ -28,8 +28,14 @@ struct Schedule {
   int target;                            // 0: every tile in one block
   int min_steps;
   int units;                             // blocks per key/value head
+  int planned;                           // the blocks of each sequence are counted by a kernel of its own
   float share;                           // 1.001 / target
 };
+
+// From more sequences than a wavefront looks through at once, their blocks are
+// counted once for all, by a kernel before the attention kernel (1024 sequences of 512
+// tokens: 185 us; looked through by every block, 402 us; 256 of them: 51 and 63).
+constexpr int kScanBatch = 64;
 
 // One sequence's share of the call.
 struct SequenceWork {
@@ -61,6 +67,13 @@ __host__ __device__ inline SequenceWork sequence_work(const AttentionArgs& a, in
   }
   if (w.steps < 1) w.steps = 1;
   return w;
+}
+
+// Where every tile is left to one block: before sequence b come at most this many
+// blocks, a number that needs no other sequence's length.
+__host__ __device__ inline int64_t tiles_before(const AttentionArgs& a, const Schedule& s, int b) {
+  const int64_t x = a.r.starts[b] < 0 ? 0 : a.r.starts[b] < a.r.rows ? a.r.starts[b] : a.r.rows;
+  return (uint32_t)(x * a.ratio) / (uint32_t)s.tile_rows + b;
 }
 
 // Steps of a block, from the steps of all tiles of one head, and a tile's chunks
@@ -118,33 +131,41 @@ constexpr int resident_blocks(int C, int groups, bool affine, int tile_rows) {
 }
 
 // The workspace: `slots` partial results for each head (the rows of a tile, then
-// for each row its reference and sum), a record for each slot, and the number of
-// slots in use.
+// for each row its reference and sum), a record for each slot, the number of slots
+// in use, and the plan of a large batch.
 struct PartRecord {
   int first, flat0, flats;               // the sequence's first row, the tile's first flat row, the sequence's flat rows
   int chunk, chunks;
   int unused[3];
 };
 
+// Blocks and slots of the sequences before one.
+struct PlanEntry {
+  int blocks, slots;
+};
+
 struct Workspace {
   float* part;
   PartRecord* record;
   int* used;
+  PlanEntry* plan;                       // [batch + 1], where planned
 };
 
 __host__ __device__ inline int64_t partial_floats(int tile_rows, int C) { return (int64_t)tile_rows * (32 * C + 2); }
 
 __host__ __device__ inline int workspace_slots(const Schedule& s) { return 2 * s.target; }
 
-inline int64_t workspace_bytes(const Schedule& s, int heads, int C) {
-  return workspace_slots(s) * (heads * partial_floats(s.tile_rows, C) * 4 + (int64_t)sizeof(PartRecord)) + 16;
+inline int64_t workspace_bytes(const Schedule& s, int heads, int C, int batch) {
+  return workspace_slots(s) * (heads * partial_floats(s.tile_rows, C) * 4 + (int64_t)sizeof(PartRecord)) + 16 +
+         (s.planned ? (batch + 1) * (int64_t)sizeof(PlanEntry) : 0);
 }
 
 __host__ __device__ inline Workspace workspace_at(void* p, const Schedule& s, int heads, int C) {
   float* const part = static_cast<float*>(p);
   PartRecord* const record =
       reinterpret_cast<PartRecord*>(part + workspace_slots(s) * (heads * partial_floats(s.tile_rows, C)));
-  return Workspace{part, record, reinterpret_cast<int*>(record + workspace_slots(s))};
+  int* const used = reinterpret_cast<int*>(record + workspace_slots(s));
+  return Workspace{part, record, used, reinterpret_cast<PlanEntry*>(used + 4)};
 }
 
 constexpr int kComputeUnits = 256;
@@ -165,6 +186,7 @@ inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   // Where no sequence can have more, every tile is left to one block and the join
   // kernel's launch is saved.
   if ((r.max_pages << c.page_shift) <= s.min_steps * kStep) s.target = 0;
+  s.planned = s.target > 0 && r.batch > kScanBatch;
   s.units = (int)(s.target + r.rows * ratio / s.tile_rows + r.batch);
   return s;
 }

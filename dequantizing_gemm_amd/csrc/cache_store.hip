@@ -58,10 +58,11 @@ __device__ __forceinline__ StoreBlock store_rows(const RowsView& r, int b) {
   return x;
 }
 
-// Steps that a sequence's rows touch. Over a batch they number at most
-// rows / 64 + 2 batch, the grid's size; without starts, one row touches one.
-__device__ __forceinline__ int store_steps(const StoreBlock& x) {
-  return x.rows > 0 ? (int)(((x.p0 + x.rows - 1) >> 6) - (x.p0 >> 6)) + 1 : 0;
+// Before sequence b come at most this many steps (n rows touch at most n / 64 + 2),
+// a number that needs no other sequence's length; the grid has them all.
+__device__ __forceinline__ int64_t steps_before(const RowsView& r, int b) {
+  const int64_t x = r.starts[b];
+  return (x < 0 ? 0 : x < r.rows ? x : r.rows) / 64 + 2 * (int64_t)b;
 }
 
 __device__ __forceinline__ bool find_store_block(const RowsView& r, int unit, StoreBlock* out) {
@@ -69,21 +70,10 @@ __device__ __forceinline__ bool find_store_block(const RowsView& r, int unit, St
     *out = store_rows(r, unit);
     return true;
   }
-  const int lane = threadIdx.x & (kWave - 1);
-  int before = 0;
-  for (int b0 = 0; b0 < r.batch; b0 += kWave) {
-    const int steps = b0 + lane < r.batch ? store_steps(store_rows(r, b0 + lane)) : 0;
-    const int upto = before + lane_scan(steps);
-    const uint64_t hit = __ballot(unit >= upto - steps && unit < upto);
-    if (hit) {
-      const int at = __builtin_ctzll(hit);
-      *out = store_rows(r, b0 + at);
-      out->base += (int64_t)(unit - __builtin_amdgcn_readlane(upto - steps, at)) * 64;
-      return true;
-    }
-    before = __builtin_amdgcn_readlane(upto, kWave - 1);
-  }
-  return false;
+  const int b = lane_search(r.batch, unit, [&](int i) { return steps_before(r, i); });
+  *out = store_rows(r, b);
+  out->base += (unit - steps_before(r, b)) * 64;
+  return out->base >= out->p0 - 63 && out->base < out->p0 + out->rows;
 }
 
 // ---------------------------------------------------------------- elements

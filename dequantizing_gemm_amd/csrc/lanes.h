@@ -1,4 +1,4 @@
-// lanes.h -- sums over a wavefront's lanes.
+// lanes.h -- sums over a wavefront's lanes, and a search by all of them.
 #pragma once
 
 #include <type_traits>
@@ -28,6 +28,23 @@ __device__ __forceinline__ T lane_scan(T v) {
 template <typename T>
 __device__ __forceinline__ T lane_value(T v, int lane) {
   return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// The last i in [0, n) with f(i) <= x, where f does not decrease; 0 if there is
+// none, and some i in range whatever f does. The lanes try 64 places at a time, so
+// that up to 64 take one load and 4096 two.
+template <typename F>
+__device__ __forceinline__ int lane_search(int n, int64_t x, F f) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int from = 0;
+  while (n > 1) {
+    const int apart = (n + kWave - 1) / kWave;
+    const uint64_t below = __ballot(lane * apart < n && f(from + lane * apart) <= x);
+    const int at = below ? 63 - __builtin_clzll(below) : 0;
+    from += at * apart;
+    n = n - at * apart < apart ? n - at * apart : apart;
+  }
+  return from;
 }
 
 }  // namespace int4dq

@@ -43,7 +43,7 @@ hipError_t launch_cache_attention(const AttentionArgs& a, void*, int64_t bytes, 
 }
 int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int ratio) {
   const Schedule s = plan_of(c, r, ratio);
-  return s.target == 0 ? 0 : workspace_bytes(s, c.heads, c.C);
+  return s.target == 0 ? 0 : workspace_bytes(s, c.heads, c.C, r.batch);
 }
 }  // namespace int4dq
 extern "C" const char* int4_last_error(void);
@@ -139,17 +139,22 @@ static void schedules() {
     CHECK(s.tile_rows != kWideRows || wide_tiles(a.c.C, a.c.C / scale_blocks(a.c), a.c.affine) > 0, "a form for prompts");
     CHECK(s.tile_rows == kWideRows || s.tile_rows <= 16 * max_tiles(a.c.C, a.c.C / scale_blocks(a.c), a.c.affine), "a tile height that has a form");
     CHECK(a.c.C % scale_blocks(a.c) == 0 && (a.c.G == 1 || a.c.group % (32 * scale_blocks(a.c)) == 0), "blocks to a scale");
-    if (trial % 5 == 4) { s.units -= s.target; s.target = 0; }
+    if (trial % 5 == 4) { s.units -= s.target; s.target = s.planned = 0; }
     {
-      void* const p = malloc((size_t)workspace_bytes(s, a.c.heads, a.c.C));
+      void* const p = malloc((size_t)workspace_bytes(s, a.c.heads, a.c.C, B));
       const Workspace ws = workspace_at(p, s, a.c.heads, a.c.C);
       *ws.used = 1;
+      if (s.planned) ws.plan[B].slots = 1;
       if (s.target > 0) {
         ws.record[0].chunk = ws.record[workspace_slots(s) - 1].chunks = 1;
         ws.part[workspace_slots(s) * (a.c.heads * partial_floats(s.tile_rows, a.c.C)) - 1] = 1.0f;
       }
       free(p);
     }
+    if (a.r.starts)
+      for (int b = 0; b < B; ++b)
+        CHECK(tiles_before(a, s, b + 1) - tiles_before(a, s, b) >= sequence_work(a, s.tile_rows, b).tiles &&
+                  tiles_before(a, s, b + 1) <= s.units, "a block for every tile");
     double all = 0;
     for (int b = 0; b < B; ++b) {
       const SequenceWork w = sequence_work(a, s.tile_rows, b);
