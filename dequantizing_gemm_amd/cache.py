@@ -147,6 +147,11 @@ class Int4Cache:
                                                           self.v_scales, self.v_zeros) if t is not None)
 
 
+def _is_cache(cache):
+    if not isinstance(cache, Int4Cache):
+        raise ValueError("cache must be an Int4Cache")
+
+
 def _int32(cache, name, t, ndim):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != ndim:
         raise ValueError(f"{name} must be an int32 tensor of {ndim} dimension(s)")
@@ -158,8 +163,6 @@ def _int32(cache, name, t, ndim):
 
 def _plan(cache, page_table, lengths, starts, rows):
     """The rows descriptor, checked; rows: what the row-wise arrays hold."""
-    if not isinstance(cache, Int4Cache):
-        raise ValueError("cache must be an Int4Cache")
     _int32(cache, "page_table", page_table, 2)
     _int32(cache, "lengths", lengths, 1)
     batch, max_pages = page_table.shape
@@ -210,6 +213,7 @@ def int4_cache_write(cache: Int4Cache, k: torch.Tensor, v: torch.Tensor, page_ta
                      lengths: torch.Tensor, starts: torch.Tensor | None = None) -> None:
     """Quantise k and v [rows, heads, head_dim] (float32, float16 or bfloat16, any
     row and head strides) into the cache at the rows' positions."""
+    _is_cache(cache)
     ks, vs = _rows_array(cache, k, "k", cache.heads), _rows_array(cache, v, "v", cache.heads)
     if k.dtype not in ROWS_DTYPES or v.dtype != k.dtype:
         raise ValueError(f"k and v must be float32, float16 or bfloat16, both the same (got {k.dtype}, {v.dtype})")
@@ -227,12 +231,13 @@ def int4_cache_read(cache: Int4Cache, page_table: torch.Tensor, lengths: torch.T
     the last starts[b+1] - starts[b] tokens of each sequence (all of them where
     that is lengths[b]). ``rows`` is starts[batch], known to the caller (default:
     one row a sequence); ``out``: a pair of contiguous tensors to fill."""
+    _is_cache(cache)
     if dtype not in ROWS_DTYPES:
         raise ValueError(f"dtype must be float32, float16 or bfloat16 (got {dtype})")
     if rows is None:
         if starts is not None and out is None:
             raise ValueError("rows must be given with starts")
-        rows = out[0].shape[0] if out is not None else lengths.shape[0]
+        rows = out[0].shape[0] if out is not None else page_table.shape[0]
     plan = _plan(cache, page_table, lengths, starts, rows)
     shape = (rows, cache.heads, cache.head_dim)
     if out is None:
@@ -258,6 +263,7 @@ def cache_attention_workspace_bytes(cache: Int4Cache, batch: int, rows: int, q_h
     """Bytes of workspace int4_cache_attention uses for these sizes: ``rows`` rows
     of ``q_heads`` query heads over ``batch`` sequences, whatever their page tables
     (a call whose table is short takes less, or none)."""
+    _is_cache(cache)
     one = None if rows == batch else 1
     most = 2 ** 31 - 1
     return _workspace_bytes(cache, _RowsStruct(None, most, most, None, one, batch, rows), q_heads)
@@ -284,6 +290,7 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
     scores (default head_dim ** -0.5). ``workspace``: a uint8 tensor from
     cache_attention_workspace; without one the call takes its scratch from
     torch's allocator."""
+    _is_cache(cache)
     q_heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
     qs = _rows_array(cache, q, "q", q_heads)
     if q.dtype not in (torch.float16, torch.bfloat16):
