@@ -908,11 +908,13 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
         asm volatile("" ::: "memory");
       };
       read_keys(0, k[0]);
+      __builtin_amdgcn_s_setprio(1);
       each<4>([&](auto nn) {
         constexpr int n = decltype(nn)::value;
         if constexpr (n < 3) read_keys(n + 1, k[(n + 1) & 1]);
         r.template score<n>(k[n & 1], sc);
       });
+      __builtin_amdgcn_s_setprio(0);
       read_values(0, v[0]);
       const bool masked = span.masks(step) || found != 15u;
       uint32_t vs[NG];
@@ -927,8 +929,10 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
         each<GC>([&](auto jj) {
           constexpr int j = g * GC + decltype(jj)::value;
           if constexpr (j + 1 < C) read_values(j + 1, v[(j + 1) & 1]);
+          __builtin_amdgcn_s_setprio(1);
           r.add(j, v[j & 1][0], v[j & 1][1], w, 0);
           r.add(j, v[j & 1][2], v[j & 1][3], w, 1);
+          __builtin_amdgcn_s_setprio(0);
         });
       });
     }
