@@ -12,32 +12,62 @@ namespace {
 // does not look through at once: one block, a thread a sequence.
 __global__ __launch_bounds__(1024) void cache_attention_plan_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
-  __shared__ float works[16];
+  __shared__ float works[2][16];
+  __shared__ int longest[16], adds[2][16];
   __shared__ PlanEntry sums[2][16];
-  float all = 0.0f;
+  const SequenceWork own = tid < a.r.batch ? sequence_work(a, sched.tile_rows, tid) : SequenceWork{};
+  auto of = [&](int b) { return b == tid ? own : sequence_work(a, sched.tile_rows, b); };
+  float work = 0.0f, tiles = 0.0f;
+  int most = 0;
   for (int b = tid; b < a.r.batch; b += 1024) {
-    const SequenceWork w = sequence_work(a, sched.tile_rows, b);
-    all += (float)w.tiles * (float)w.steps;
+    const SequenceWork w = of(b);
+    work += (float)w.tiles * (float)w.steps;
+    tiles += (float)w.tiles;
+    most = w.tiles > 0 && w.steps > most ? w.steps : most;
   }
-  all = lane_scan(all);
-  if (lane == kWave - 1) works[wave] = all;
+  work = lane_scan(work);
+  tiles = lane_scan(tiles);
+  most = lane_max(most);
+  if (lane == kWave - 1) {
+    works[0][wave] = work;
+    works[1][wave] = tiles;
+    longest[wave] = most;
+  }
   __syncthreads();
-  all = 0.0f;
-  for (int i = 0; i < 16; ++i) all += works[i];
-  const float each_step = blocks_per_step(sched, all);
+  work = tiles = 0.0f;
+  for (int i = 0; i < 16; ++i) {
+    work += works[0][i];
+    tiles += works[1][i];
+    most = longest[i] > most ? longest[i] : most;
+  }
+  int turn = 0;
+  const int per = steps_per_block(sched, work, tiles, most, [&](int x) {
+    int sum = 0;
+    for (int b = tid; b < a.r.batch; b += 1024) {
+      const SequenceWork w = of(b);
+      sum += w.tiles > 0 ? (chunks_of(w.steps, x) - 1) * w.tiles : 0;
+    }
+    sum = lane_scan(sum);
+    if (lane == kWave - 1) adds[turn][wave] = sum;
+    __syncthreads();                     // two buffers: the one written next was read before this
+    sum = 0;
+    for (int i = 0; i < 16; ++i) sum += adds[turn][i];
+    turn ^= 1;
+    return sum;
+  });
   int blocks = 0, slots = 0;
-  for (int b0 = 0, turn = 0; b0 < a.r.batch; b0 += 1024, turn ^= 1) {
+  for (int b0 = 0; b0 < a.r.batch; b0 += 1024, turn ^= 1) {
     const int b = b0 + tid;
     int mine = 0, mine_slots = 0;
     if (b < a.r.batch) {
-      const SequenceWork w = sequence_work(a, sched.tile_rows, b);
-      const int chunks = chunks_of(w.steps, each_step);
+      const SequenceWork w = of(b);
+      const int chunks = w.tiles > 0 ? chunks_of(w.steps, per) : 0;
       mine = chunks * w.tiles;
       mine_slots = chunks > 1 ? mine : 0;
     }
     int upto = lane_scan(mine), slots_upto = lane_scan(mine_slots);
     if (lane == kWave - 1) sums[turn][wave] = PlanEntry{upto, slots_upto};
-    __syncthreads();                     // two buffers: the one written next was read before this
+    __syncthreads();                     // (two buffers here too)
     upto += blocks;
     slots_upto += slots;
     for (int i = 0; i < 16; ++i) {
@@ -166,7 +196,12 @@ int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int rat
 
 hipError_t launch_cache_attention(const AttentionArgs& a, void* workspace, int64_t bytes, hipStream_t stream) {
   Schedule s = plan_of(a.c, a.r, a.ratio);
-  if (bytes < cache_attention_workspace(a.c, a.r, a.ratio)) {
+  auto fits = [&] { return s.target == 0 || bytes >= workspace_bytes(s, a.c.heads, a.c.C, a.r.batch); };
+  if (s.crowded && !fits()) {            // a workspace made for a larger call may have room for fewer cuts
+    s.units -= s.target;
+    s.crowded = 0;
+  }
+  if (!fits()) {
     s.units -= s.target;
     s.target = s.planned = 0;
   }

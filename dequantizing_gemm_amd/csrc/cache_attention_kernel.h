@@ -87,8 +87,12 @@ __device__ __forceinline__ bool find_block(const AttentionArgs& a, const Schedul
   *used = 0;
   if (s.target > 0 && !s.planned) {      // all sequences at once
     const SequenceWork w = lane < a.r.batch ? sequence_work(a, s.tile_rows, lane) : SequenceWork{};
-    const float all = lane_value(lane_scan((float)w.tiles * (float)w.steps), kWave - 1);
-    const int chunks = w.tiles > 0 ? chunks_of(w.steps, blocks_per_step(s, all)) : 0;
+    const float work = lane_value(lane_scan((float)w.tiles * (float)w.steps), kWave - 1);
+    const float tiles = lane_value(lane_scan((float)w.tiles), kWave - 1);
+    const int per = steps_per_block(s, work, tiles, lane_max(w.tiles > 0 ? w.steps : 0), [&](int x) {
+      return lane_value(lane_scan(w.tiles > 0 ? (chunks_of(w.steps, x) - 1) * w.tiles : 0), kWave - 1);
+    });
+    const int chunks = w.tiles > 0 ? chunks_of(w.steps, per) : 0;
     const int mine = chunks * w.tiles, mine_slots = chunks > 1 ? mine : 0;
     const int upto = lane_scan(mine), slots_upto = lane_scan(mine_slots);
     *used = lane_value(slots_upto, kWave - 1);
@@ -632,7 +636,7 @@ struct Span {
 // query rows. The block's four wavefronts take turns on the steps; their results
 // are joined through LDS.
 template <int C, int GC, int QT, bool AFF>
-__global__ __launch_bounds__(256) void cache_attention_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
+__global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void cache_attention_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
   constexpr int NG = C / GC, DB = 16 * C, TR = 16 * QT;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform

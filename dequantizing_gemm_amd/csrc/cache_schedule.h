@@ -3,16 +3,17 @@
 // A sequence with n rows gives n * ratio query rows per key/value head (row i,
 // head r of the head's `ratio` query heads: flat row i * ratio + r), cut into
 // tiles of tile_rows. A tile sees a run of keys, cut into steps of 64 tokens;
-// the steps of a tile are shared out over `chunks` blocks. How many is decided
-// on the GPU from the lengths: with W the steps of all tiles of one head and
-// `target` the blocks per head that fill the GPU, a block takes about
-// per_block = max(min_steps, 1.001 W / target) steps, so a long sequence gets many
-// blocks and a short one a single one, whatever mixture the batch is. Hence
-//   blocks per head <= W / per_block + tiles <= target + tiles
-// (the size of the grid, known on the host), and the blocks of tiles with more
-// than one chunk, which leave partial results in the workspace, number at most
-// 2 target: such a tile has over per_block steps, so there are at most target of
-// them.
+// the steps of a tile are shared out over `chunks` blocks of equal length. How many
+// is decided on the GPU from the lengths, whatever mixture the batch is: `target`
+// blocks per head fill the GPU once, and the longest block is made as short as
+// their number allows (steps_per_block), so that all run at once and end together;
+// with more tiles than that, tiles are cut down to the average share; and with a
+// few more, which would leave most of the GPU idle for their length, all are cut
+// further, to at most 3 target blocks (149 tiles and a target of 128: 4 prompts in chunks, 253 us
+// uncut, 234 so).
+// So cuts add at most `target` blocks, and a tile of c > 1 chunks adds
+// c - 1 >= c / 2 of them, or the blocks are at most 3 target: that bounds the grid
+// and the number of partial results, which the host has to know.
 #pragma once
 
 #include "cache.h"
@@ -28,8 +29,8 @@ struct Schedule {
   int target;                            // 0: every tile in one block
   int min_steps;
   int units;                             // blocks per key/value head
+  int crowded;                           // tiles may be more than the target by up to half
   int planned;                           // the blocks of each sequence are counted by a kernel of its own
-  float share;                           // 1.001 / target
 };
 
 // From more sequences than a wavefront looks through at once, their blocks are
@@ -76,17 +77,30 @@ __host__ __device__ inline int64_t tiles_before(const AttentionArgs& a, const Sc
   return (uint32_t)(x * a.ratio) / (uint32_t)s.tile_rows + b;
 }
 
-// Steps of a block, from the steps of all tiles of one head, and a tile's chunks
-// with that. Binary32 arithmetic, the same in every kernel; the margin in `share`
-// covers its rounding, so that the bounds above hold.
-__host__ __device__ inline float blocks_per_step(const Schedule& s, float all_steps) {
-  if (s.target == 0) return 0.0f;
-  const float per = all_steps * s.share;
-  return 1.0f / (per < (float)s.min_steps ? (float)s.min_steps : per);
-}
+// Chunks of a tile when no block takes more than `per` steps.
+__host__ __device__ inline int chunks_of(int steps, int per) { return (int)((uint32_t)(steps + per - 1) / (uint32_t)per); }
 
-__host__ __device__ inline int chunks_of(int steps, float blocks_per_step) {
-  return (int)((float)(steps - 1) * blocks_per_step) + 1;
+// The fewest steps for the longest block with which the cuts add no more blocks
+// than there is room for: what `tiles` leave of the target, or the target where they
+// exceed it (by much). `work`: the steps of all tiles of one head, `most` those of the
+// longest; added(per): the blocks that chunks_of adds with `per`, at most
+// work / per, so that work / room is enough (1.001: the sum's rounding).
+template <typename F>
+__host__ __device__ inline int steps_per_block(const Schedule& s, float work, float tiles, int most, F added) {
+  const bool fits = tiles <= (float)s.target, few_over = !fits && s.crowded && tiles <= 1.5f * (float)s.target;
+  const int room = fits ? s.target - (int)tiles : few_over ? 3 * s.target - (int)tiles : s.target;
+  int from = (int)(work / (float)(few_over ? 3 * s.target : s.target)), to = most;
+  if (from < s.min_steps) from = s.min_steps;
+  if (room > 0) {
+    const float enough = work * 1.001f / (float)room + 1.0f;
+    if (enough < (float)to) to = (int)enough;
+  }
+  while (from < to) {
+    const int per = (int)(((uint32_t)from + (uint32_t)to) / 2);
+    if (added(per) <= room) to = per;
+    else from = per + 1;
+  }
+  return from;
 }
 
 // Keys [lo, hi) that row `token` of a sequence's rows sees.
@@ -123,11 +137,12 @@ constexpr int wide_tiles(int C, int groups, bool affine) {
   return groups * C >= (affine ? 32 : 64) ? 0 : C <= 4 && !(affine && groups > 1) ? 2 : 1;      // 0: no such form
 }
 
-// Blocks of a form that a CU holds at once, by their registers and LDS.
+// Blocks of a form that a CU holds at once, by their registers and LDS; the form for
+// few rows is compiled to fit that many.
 constexpr int resident_blocks(int C, int groups, bool affine, int tile_rows) {
   if (tile_rows == kWideRows) return wide_tiles(C, groups, affine);              // of 4 wavefronts, or 1 of 8
-  if (tile_rows == 32) return C == 2 && !affine ? 3 : 2;
-  return C == 2 ? 4 : C == 3 ? 3 : C == 4 ? (affine && groups > 2 ? 2 : 3) : groups * C >= (affine ? 32 : 64) ? 1 : 2;
+  if (tile_rows == 32) return C == 2 && !affine && groups == 1 ? 3 : 2;
+  return C == 2 ? 4 : C == 3 ? (groups == 1 && !affine ? 4 : 3) : C == 4 ? (groups > 2 ? 2 : 3) : groups * C >= (affine ? 32 : 64) ? 1 : 2;
 }
 
 // The workspace: `slots` partial results for each head (the rows of a tile, then
@@ -153,7 +168,7 @@ struct Workspace {
 
 __host__ __device__ inline int64_t partial_floats(int tile_rows, int C) { return (int64_t)tile_rows * (32 * C + 2); }
 
-__host__ __device__ inline int workspace_slots(const Schedule& s) { return 2 * s.target; }
+__host__ __device__ inline int workspace_slots(const Schedule& s) { return (s.crowded ? 3 : 2) * s.target; }
 
 inline int64_t workspace_bytes(const Schedule& s, int heads, int C, int batch) {
   return workspace_slots(s) * (heads * partial_floats(s.tile_rows, C) * 4 + (int64_t)sizeof(PartRecord)) + 16 +
@@ -181,13 +196,14 @@ inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   s.tile_rows = wide ? kWideRows : mean <= 16 ? 16 : most;
   const int resident = resident_blocks(c.C, groups, c.affine, s.tile_rows);
   s.target = (resident * kComputeUnits + c.heads - 1) / c.heads;
-  s.share = 1.001f / (float)s.target;
   s.min_steps = 16;                      // four for each wavefront of the form for few rows
   // Where no sequence can have more, every tile is left to one block and the join
   // kernel's launch is saved.
   if ((r.max_pages << c.page_shift) <= s.min_steps * kStep) s.target = 0;
   s.planned = s.target > 0 && r.batch > kScanBatch;
-  s.units = (int)(s.target + r.rows * ratio / s.tile_rows + r.batch);
+  const int64_t fewest = (r.rows * ratio + s.tile_rows - 1) / s.tile_rows, tiles = r.rows * ratio / s.tile_rows + r.batch;
+  s.crowded = tiles > s.target && 2 * fewest <= 3 * (int64_t)s.target;
+  s.units = (int)(s.target * (s.crowded ? 2 : 1) + tiles);
   return s;
 }
 

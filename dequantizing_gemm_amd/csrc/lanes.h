@@ -30,6 +30,16 @@ __device__ __forceinline__ T lane_value(T v, int lane) {
   return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 
+// The largest over the lanes, of numbers from 0 up.
+__device__ __forceinline__ int lane_max(int v) {
+#pragma unroll
+  for (int x = 1; x < kWave; x <<= 1) {
+    const int o = __shfl_xor(v, x);
+    v = o > v ? o : v;
+  }
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
 // The last i in [0, n) with f(i) <= x, where f does not decrease; 0 if there is
 // none, and some i in range whatever f does. The lanes try 64 places at a time, so
 // that up to 64 take one load and 4096 two.

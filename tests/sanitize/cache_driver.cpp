@@ -139,7 +139,7 @@ static void schedules() {
     CHECK(s.tile_rows != kWideRows || wide_tiles(a.c.C, a.c.C / scale_blocks(a.c), a.c.affine) > 0, "a form for prompts");
     CHECK(s.tile_rows == kWideRows || s.tile_rows <= 16 * max_tiles(a.c.C, a.c.C / scale_blocks(a.c), a.c.affine), "a tile height that has a form");
     CHECK(a.c.C % scale_blocks(a.c) == 0 && (a.c.G == 1 || a.c.group % (32 * scale_blocks(a.c)) == 0), "blocks to a scale");
-    if (trial % 5 == 4) { s.units -= s.target; s.target = s.planned = 0; }
+    if (trial % 5 == 4) { s.units -= s.target * (s.crowded ? 2 : 1); s.target = s.crowded = s.planned = 0; }
     {
       void* const p = malloc((size_t)workspace_bytes(s, a.c.heads, a.c.C, B));
       const Workspace ws = workspace_at(p, s, a.c.heads, a.c.C);
@@ -155,13 +155,28 @@ static void schedules() {
       for (int b = 0; b < B; ++b)
         CHECK(tiles_before(a, s, b + 1) - tiles_before(a, s, b) >= sequence_work(a, s.tile_rows, b).tiles &&
                   tiles_before(a, s, b + 1) <= s.units, "a block for every tile");
-    double all = 0;
+    double all = 0, tiles = 0;
+    int most_steps = 0;
     for (int b = 0; b < B; ++b) {
       const SequenceWork w = sequence_work(a, s.tile_rows, b);
       all += (double)w.tiles * w.steps;
+      tiles += w.tiles;
+      if (w.tiles > 0 && w.steps > most_steps) most_steps = w.steps;
     }
     for (const double off : {1.0 - 3e-5, 1.0, 1.0 + 3e-5}) {     // binary32 sums in some order
-      const float per = blocks_per_step(s, (float)(all * off));
+      if (s.target == 0 && off != 1.0) continue;
+      auto added = [&](int x) {
+        int sum = 0;
+        for (int b = 0; b < B; ++b) {
+          const SequenceWork w = sequence_work(a, s.tile_rows, b);
+          if (w.tiles > 0) sum += (chunks_of(w.steps, x) - 1) * w.tiles;
+        }
+        return sum;
+      };
+      const int per = s.target == 0 ? INT32_MAX / 2 : steps_per_block(s, (float)(all * off), (float)tiles, most_steps, added);
+      CHECK(per >= s.min_steps, "the least share");
+      if (s.target > 0)
+        CHECK(added(per) <= (tiles <= s.target ? s.target - (int)tiles : s.crowded ? 2 * s.target : s.target), "room for the cuts");
       int64_t blocks = 0, slots = 0, rows = 0;
       for (int b = 0; b < B; ++b) {
         const SequenceWork w = sequence_work(a, s.tile_rows, b);

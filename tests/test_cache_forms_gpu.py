@@ -109,6 +109,27 @@ def test_many_sequences(dq, batch, long_at, one_row):
     check_attention(dq, m, table, lengths, None if one_row else starts, q, F16, cache=cache)
 
 
+@pytest.mark.parametrize("heads,ratio,batch,rows,longs", [(32, 1, 26, 1, 3), (11, 2, 80, 1, 5), (32, 1, 20, 3, 4), (32, 2, 9, 125, 1)])
+def test_a_few_more_tiles_than_fit(dq, heads, ratio, batch, rows, longs):
+    """Somewhat more tiles than the GPU holds at once, some of them cut; and the same
+    call with a workspace that has no room for as many cuts."""
+    rng = np.random.default_rng(50 + batch)
+    lengths = rng.integers(rows, rows + 9, size=batch)
+    lengths[rng.permutation(batch)[:longs]] = 1100 + rng.integers(0, 200, size=longs)
+    D = 128 if rows < 100 else 64
+    say("case: crowded", heads, ratio, batch, rows)
+    m, table, starts = filled(rng, heads, D, D, False, 16, lengths, [rows] * batch)
+    q = rounded(rng.normal(size=(int(starts[-1]), heads * ratio, D)).astype(np.float32), BF16)
+    cache, st = cache_of(dq, m), None if rows == 1 else starts
+    n = dq.cache_attention_workspace_bytes(cache, batch, len(q), heads * ratio)
+    out, lse = check_attention(dq, m, table, lengths, st, q, BF16, cache=cache)
+    if rows > 100:
+        return
+    for room in (n * 2 // 3 + 256 * batch, n // 2):
+        ws = torch.full((room,), 0x7F, dtype=torch.uint8, device=DEV)
+        check_attention(dq, m, table, lengths, st, q, BF16, cache=cache, workspace=ws)
+
+
 def test_many_query_heads_of_one(dq):
     """33 query heads to a key/value head and one row a sequence: several tiles a row."""
     rng = np.random.default_rng(31)
