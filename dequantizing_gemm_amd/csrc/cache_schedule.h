@@ -9,8 +9,8 @@
 // their number allows (steps_per_block), so that all run at once and end together;
 // with more tiles than that, tiles are cut down to the average share; and with a
 // few more, which would leave most of the GPU idle for their length, all are cut
-// further, to at most 3 target blocks (149 tiles and a target of 128: 4 prompts in chunks, 253 us
-// uncut, 234 so).
+// further, to at most 3 target blocks (4 prompts in chunks, 149 tiles and a target of
+// 128: 253 us uncut, 234 so).
 // So cuts add at most `target` blocks, and a tile of c > 1 chunks adds
 // c - 1 >= c / 2 of them, or the blocks are at most 3 target: that bounds the grid
 // and the number of partial results, which the host has to know.
@@ -186,17 +186,23 @@ __host__ __device__ inline Workspace workspace_at(void* p, const Schedule& s, in
 constexpr int kComputeUnits = 256;
 
 // Tiles of 16 rows for token generation, of 32 where the sequences' rows fill
-// them, the form for prompts from more rows than one of its tiles holds (8 sequences
-// of 2650 tokens on average: 96 rows 39 us against its 48, 128 rows 43 against 51).
+// them, and the form for prompts where a sequence's rows fill a tile of it, or two
+// where tiles of 32 are the other choice. Measured on 8 sequences of 2650 tokens on
+// average, 8 key/value heads, few rows' form and prompts': head width 128, 128 rows
+// 39 us and 52, 256 rows 60 and 60, 512 rows 91 and 90; width 256 (tiles of 16),
+// 128 rows 69 and 71, 192 rows 96 and 90.
 inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   Schedule s{};
   const int64_t mean = (r.rows * ratio + r.batch - 1) / r.batch;
   const int groups = c.C / scale_blocks(c), most = 16 * max_tiles(c.C, groups, c.affine);
-  const bool wide = mean > kWideRows && wide_tiles(c.C, groups, c.affine) > 0;
+  const bool wide = mean > most / 16 * kWideRows && wide_tiles(c.C, groups, c.affine) > 0;
   s.tile_rows = wide ? kWideRows : mean <= 16 ? 16 : most;
   const int resident = resident_blocks(c.C, groups, c.affine, s.tile_rows);
   s.target = (resident * kComputeUnits + c.heads - 1) / c.heads;
-  s.min_steps = 16;                      // four for each wavefront of the form for few rows
+  // Four for each wavefront of the form for few rows (16 sequences of 2650 tokens, 3 to
+  // 6 rows each, with at least one each: 40 us, four: 35; one row of 2000 tokens 18.7
+  // and 17.7).
+  s.min_steps = 16;
   // Where no sequence can have more, every tile is left to one block and the join
   // kernel's launch is saved.
   if ((r.max_pages << c.page_shift) <= s.min_steps * kStep) s.target = 0;

@@ -29,10 +29,10 @@ PROMPTS = [  # D, group, affine, heads, ratio, dtype, window
 
 @pytest.mark.parametrize("D,group,affine,heads,ratio,dtype,window", PROMPTS)
 def test_prompts(dq, D, group, affine, heads, ratio, dtype, window):
-    """More than 128 query rows a key/value head and sequence on average, a tile that
+    """More than 256 query rows a key/value head and sequence on average, a tile that
     ends inside, one sequence that continues what is cached and one that is new."""
     rng = np.random.default_rng(1000 + D + group + window)
-    lengths, new = [150, 210, 3], [75, 210, 1]
+    lengths, new = [230, 290, 3], [140, 290, 3]
     say("case: prompts", D, group, affine, heads, ratio, dtype, window)
     m, table, starts = filled(rng, heads, D, group, affine, 32, lengths, new)
     q = rounded(rng.normal(size=(int(starts[-1]), heads * ratio, D)).astype(np.float32), dtype)
@@ -54,9 +54,11 @@ LONG = [  # D, group, affine, heads, ratio, page, dtype, lengths, new rows, wind
     (128, 128, False, 1, 2, 128, F16, [1900], [90], 0),
     (64, 32, True, 1, 2, 64, BF16, [2100, 1300], [100, 70], 1200),
     (256, 64, False, 1, 1, 64, F16, [1400], [140], 0),
+    (128, 128, False, 1, 2, 128, F16, [1900], [150], 0),
+    (64, 32, True, 1, 3, 64, BF16, [2100, 1300], [100, 90], 1200),
     (64, 64, False, 1, 2, 64, BF16, [9300], [1], 0),
     (64, 64, False, 1, 2, 64, F16, [9300, 5], [70, 1], 0),
-    (64, 64, True, 1, 2, 256, F16, [9300], [130], 0),
+    (64, 64, True, 1, 2, 256, F16, [9300], [130], 0), (64, 64, False, 1, 2, 256, F16, [9300], [140], 0),
 ]
 
 
@@ -109,7 +111,7 @@ def test_many_sequences(dq, batch, long_at, one_row):
     check_attention(dq, m, table, lengths, None if one_row else starts, q, F16, cache=cache)
 
 
-@pytest.mark.parametrize("heads,ratio,batch,rows,longs", [(32, 1, 26, 1, 3), (11, 2, 80, 1, 5), (32, 1, 20, 3, 4), (32, 2, 9, 125, 1)])
+@pytest.mark.parametrize("heads,ratio,batch,rows,longs", [(32, 1, 26, 1, 3), (11, 2, 80, 1, 5), (32, 1, 20, 3, 4), (32, 2, 9, 125, 1), (32, 2, 7, 130, 1)])
 def test_a_few_more_tiles_than_fit(dq, heads, ratio, batch, rows, longs):
     """Somewhat more tiles than the GPU holds at once, some of them cut; and the same
     call with a workspace that has no room for as many cuts."""
@@ -237,7 +239,7 @@ def test_refusals(dq):
     refused(w, c, k, k, table, lens[:1], match="lengths has 1")
     refused(w, c, k, k, table, lens, starts[:2], match="starts has 2")
     refused(w, c, k, k, table, lens, starts.float(), match="starts must be an int32")
-    refused(w, "cache", k, k, table, lens, match="")
+    refused(w, "cache", k, k, table, lens, match="Int4Cache")
     refused(r, c, table, lens, starts, match="rows must be given")
     refused(r, c, table, lens, dtype=torch.int8, match="dtype must be")
     refused(r, c, table, lens, rows=3, match="one row a sequence")
