@@ -35,7 +35,15 @@
 // tokens' value codes comes apart. The codes come from memory straight
 // into the operand's lanes (see the layouts in include/int4dq_cache.h), 16
 // bytes a lane for 128 channels, with the next step's loads in flight while
-// this one's are used; no LDS in the loop.
+// this one's are used; no LDS in the loop. For prompts the codes are taken apart
+// once a block instead, and shared through LDS (see the second kernel).
+//
+// What bounds it (8 key/value heads of 128 channels, 32 query heads). Token
+// generation, 64 sequences of 130 to 8190 tokens, groups of 64, bfloat16: memory, 295
+// MB in 67 us. One sequence of 131071 tokens, groups of 32 with zero points: the
+// VALU, which takes codes apart and applies scales; 159 MB in 50 us. A prompt of
+// 4096 tokens: 137 GFLOP in 188 us, the VALU busy for 54% of it and the matrix pipes
+// for 27%, with little overlap at two wavefronts a SIMD.
 #pragma once
 
 #include <type_traits>
@@ -636,7 +644,8 @@ struct Span {
 // query rows. The block's four wavefronts take turns on the steps; their results
 // are joined through LDS.
 template <int C, int GC, int QT, bool AFF>
-__global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void cache_attention_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
+__global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void cache_attention_kernel(
+    AttentionArgs a, Schedule sched, Workspace ws) {
   constexpr int NG = C / GC, DB = 16 * C, TR = 16 * QT;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform

@@ -2,8 +2,12 @@
 // them back (include/int4dq_cache.h).
 //
 // Mathematics: the group quantizer of quantize.hip on rows of head_dim
-// channels, one row per (token, head) of the keys and of the values. Bound by
-// memory.
+// channels, one row per (token, head) of the keys and of the values. Reading back
+// is bound by memory (4 sequences of 9001 to 40961 tokens, 8 heads of 128, to
+// bfloat16: 679 MB in 186 us, 3.7 TB/s), writing by the rounding's instructions (12
+// prompts of 300 to 4100 tokens, 8 heads of 128, groups of 32 with zero points, from
+// bfloat16: 57 us, the VALU busy for 70% of it), one token of one sequence by the
+// chain of dependent loads (5 us either way).
 //
 // Work decomposition: a block of 256 threads takes 64 positions (a step: four of
 // the cache's 16-token units) of a sequence, blockIdx.z the keys or the values, for

@@ -95,8 +95,11 @@ int64_t int4_cache_row_bytes(int64_t head_dim);
  *                was. Codes of the channels that pad head_dim to 32 C are 0.
  * Errors: EINVAL for a NULL pointer, a size out of range or that overflows,
  * heads > 65535, a group below head_dim other than 32, 64, 128, a page_size
- * that is no power of two from 16 to 2^20, one of k_zeros / v_zeros only, a misaligned cache array, an unknown dtype, a stride beyond
- * 2^30, rows != batch with starts = NULL. rows = 0 or batch = 0 is a valid no-op.
+ * that is no power of two from 16 to 2^20, 2^31 or more units of 16 tokens and one
+ * head in the cache, one of k_zeros / v_zeros only, a misaligned cache array, an
+ * unknown dtype, a stride beyond 2^30, batch above 2^22, rows above 2^26, a
+ * table_stride below max_pages, rows != batch with starts = NULL. rows = 0 or
+ * batch = 0 is a valid no-op.
  */
 int int4_cache_write(const int4_cache_t *cache, const int4_cache_rows_t *rows, const void *k,
                      int64_t k_row_stride, int64_t k_head_stride, const void *v,
@@ -133,7 +136,8 @@ int int4_cache_read(const int4_cache_t *cache, const int4_cache_rows_t *rows, vo
  *   workspace: device memory, 256-byte aligned, any contents, of at least
  *                int4_cache_attention_workspace_bytes, which lets long sequences
  *                be shared out over the whole GPU; or NULL with
- *                workspace_bytes = 0, and any smaller size runs without that.
+ *                workspace_bytes = 0, and any smaller size runs without that or
+ *                with less of it.
  *                Calls that share a workspace must not overlap.
  * Preconditions not checked: q is finite and below 2^100 in magnitude.
  * Errors: those of int4_cache_write, and EINVAL for q_heads that is no multiple
@@ -149,7 +153,8 @@ int int4_cache_attention(const int4_cache_t *cache, const int4_cache_rows_t *row
 /*
  * Workspace bytes of int4_cache_attention for these sizes (no pointer in the
  * descriptors is read or has to be set, except that starts = NULL says one row
- * a sequence and k_zeros = NULL symmetric codes); 0: the call does not use one. -1 on invalid sizes.
+ * a sequence and k_zeros = NULL symmetric codes); 0: the call does not use one.
+ * -1 on invalid sizes.
  */
 int64_t int4_cache_attention_workspace_bytes(const int4_cache_t *cache,
                                              const int4_cache_rows_t *rows, int64_t q_heads);
