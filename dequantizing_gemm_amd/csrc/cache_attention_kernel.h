@@ -42,8 +42,8 @@
 // generation, 64 sequences of 130 to 8190 tokens, groups of 64, bfloat16: memory, 295
 // MB in 67 us. One sequence of 131071 tokens, groups of 32 with zero points: the
 // VALU, which takes codes apart and applies scales; 159 MB in 50 us. A prompt of
-// 4096 tokens: 137 GFLOP in 188 us, the VALU busy for 54% of it and the matrix pipes
-// for 27%, with little overlap at two wavefronts a SIMD.
+// 4096 tokens: 137 GFLOP in 188 us, the VALU busy for 56% of it and the matrix pipes
+// for 28%, with little overlap at two wavefronts a SIMD.
 #pragma once
 
 #include <type_traits>

@@ -6,7 +6,7 @@
 // is bound by memory (4 sequences of 9001 to 40961 tokens, 8 heads of 128, to
 // bfloat16: 679 MB in 186 us, 3.7 TB/s), writing by the rounding's instructions (12
 // prompts of 300 to 4100 tokens, 8 heads of 128, groups of 32 with zero points, from
-// bfloat16: 57 us, the VALU busy for 70% of it), one token of one sequence by the
+// bfloat16: 57 us, the VALU busy for 73% of it), one token of one sequence by the
 // chain of dependent loads (5 us either way).
 //
 // Work decomposition: a block of 256 threads takes 64 positions (a step: four of
