@@ -279,7 +279,7 @@ struct PageTable {
     Pages r;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int index = (step * kStep + 16 * u) >> shift;
+      const int index = (int)(unit_token(step, u) >> shift);
       r.p[u] = table[index < last ? index : last];
     }
     return r;
@@ -290,7 +290,7 @@ struct PageTable {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool ok = (uint32_t)x.p[u] < (uint32_t)pages;
-      r.at[u] = ok ? x.p[u] * page_units + head_unit + (((step * kStep + 16 * u) & slots) >> 4) : 0;
+      r.at[u] = ok ? x.p[u] * page_units + head_unit + (int)((unit_token(step, u) & (uint32_t)slots) >> 4) : 0;
       r.found |= ok ? 1u << u : 0u;
     }
     return r;
@@ -632,10 +632,7 @@ struct Span {
     visible(a, w, (uint32_t)flat0 / (uint32_t)a.ratio, &lo_first, &hi_first);
     visible(a, w, (uint32_t)((flat0 + n < flats ? flat0 + n : flats) - 1) / (uint32_t)a.ratio, &lo_last, &hi_last);
   }
-  // Whether some row does not see some token of the step.
-  __device__ __forceinline__ bool masks(int step) const {
-    return step * kStep < lo_last || (step + 1) * kStep > hi_first;
-  }
+  __device__ __forceinline__ bool masks(int step) const { return step_masked(step, lo_last, hi_first); }
 };
 
 // ---------------------------------------------------------------- few rows

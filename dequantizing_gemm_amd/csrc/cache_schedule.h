@@ -38,6 +38,16 @@ struct Schedule {
 // tokens: 185 us; looked through by every block, 402 us; 256 of them: 51 and 63).
 constexpr int kScanBatch = 64;
 
+// The first token of the 16-token unit u of a step. Unsigned: loads run a few steps
+// ahead, past 2^31 where a sequence ends just below.
+__host__ __device__ inline uint32_t unit_token(int step, int u) { return (uint32_t)step * kStep + 16u * (uint32_t)u; }
+
+// Whether some row of a tile does not see some token of the step, where all rows see
+// keys [lo, hi).
+__host__ __device__ inline bool step_masked(int step, int lo, int hi) {
+  return unit_token(step, 0) < (uint32_t)lo || unit_token(step + 1, 0) > (uint32_t)hi;
+}
+
 // One sequence's share of the call.
 struct SequenceWork {
   int first;                             // its first row
@@ -63,8 +73,8 @@ __host__ __device__ inline SequenceWork sequence_work(const AttentionArgs& a, in
   w.steps = w.keys / kStep + (w.keys % kStep != 0);
   if (a.window > 0 && a.window < w.keys) {
     // a tile's rows lie on at most tile_rows / ratio + 2 positions
-    const int run = ((int)a.window + tile_rows / a.ratio + 2) / kStep + 2;
-    if (run < w.steps) w.steps = run;
+    const int64_t run = (a.window + tile_rows / a.ratio + 2) / kStep + 2;
+    if (run < w.steps) w.steps = (int)run;
   }
   if (w.steps < 1) w.steps = 1;
   return w;

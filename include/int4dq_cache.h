@@ -139,7 +139,8 @@ int int4_cache_read(const int4_cache_t *cache, const int4_cache_rows_t *rows, vo
  *                workspace_bytes = 0, and any smaller size runs without that or
  *                with less of it.
  *                Calls that share a workspace must not overlap.
- * Preconditions not checked: q is finite and below 2^100 in magnitude.
+ * Preconditions not checked: q is finite and below 2^100 in magnitude, and so are
+ * the scores a_j below 2^96.
  * Errors: those of int4_cache_write, and EINVAL for q_heads that is no multiple
  * of heads, a scale that is not finite and above 0, window < 0 or window
  * without causal, a bad workspace, INT4DQ_ROWS_F32, rows * q_heads above 2^27 or

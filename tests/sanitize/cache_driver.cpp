@@ -212,6 +212,30 @@ static void schedules() {
   }
 }
 
+// A sequence of 2^31 - 1 tokens: its last steps, and those that loads ask for ahead.
+static void the_longest() {
+  AttentionArgs a{};
+  a.c = view(64, 64, 1, 4, 1);
+  a.ratio = 1;
+  a.causal = 1;
+  const int32_t length = INT32_MAX, last = INT32_MAX / kStep;
+  a.r = RowsView{nullptr, 1 << 27, 1 << 27, &length, nullptr, 1, 1};
+  for (const int64_t window : {(int64_t)0, (int64_t)INT32_MAX - 1, (int64_t)INT32_MAX, (int64_t)1 << 40, (int64_t)100}) {
+    a.window = window;
+    const SequenceWork w = sequence_work(a, 16, 0);
+    CHECK(w.keys == INT32_MAX && w.steps >= 1 && w.steps <= last + 1, "steps of the longest sequence");
+    CHECK(window == 100 ? w.steps < 8 : w.steps == last + 1, "a window as long as the sequence");
+    int lo, hi, begin, end;
+    visible(a, w, 0, &lo, &hi);
+    chunk_steps(lo, hi, 6, 7, &begin, &end);
+    CHECK(end == last + 1 && hi == INT32_MAX, "its last chunk");
+    CHECK(step_masked(last, lo, hi) && !step_masked(last - 1, lo - (window == 100 ? 200 : 0), hi), "the last step is masked");
+  }
+  for (int ahead = 0; ahead <= 8; ++ahead)
+    for (int u = 0; u < 4; ++u)
+      CHECK(unit_token(last + ahead, u) >> 4 == ((uint64_t)(last + ahead) * kStep + 16 * u) >> 4, "units ahead of the end");
+}
+
 static void refusals() {
   alignas(256) static unsigned char arena[4096];
   int4_cache_t c{arena, (uint16_t*)arena, nullptr, arena, (uint16_t*)arena, nullptr, 4, 64, 2, 128, 64};
@@ -306,6 +330,7 @@ int main() {
   refusals();
   rows_and_pages();
   schedules();
+  the_longest();
   if (failures) return 1;
   printf("all checks passed\n");
   return 0;

@@ -210,6 +210,28 @@ def test_graphs_that_share_a_workspace(dq, rows, batch):
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), n
 
 
+def test_the_longest_sequence(dq):
+    """2^31 - 1 tokens, all pages the same 16: the softmax is theirs, its sum 2^27
+    times as large (2^-27 less for the missing token). A wavefront adds up
+    N = 2^25 / 4096 steps (1024 blocks of four), 16 probabilities and 2 products of
+    each in binary32: 18 N 2^-24 relative at most, beside the usual bound."""
+    rng = np.random.default_rng(60)
+    m = Model(1, 16, 1, 64, 64, False, fill=0x7E)
+    small = np.zeros((1, 1), np.int32)
+    m.write(values(rng, 16, 1, 64), values(rng, 16, 1, 64), small, [16], np.array([0, 16], np.int32))
+    q = rounded(rng.normal(size=(1, 2, 64)).astype(np.float32), F16)
+    ref, rlse, _, tol, ltol = m.attend(q, small, np.array([16]), None, 0.125)
+    table = torch.zeros(1, 1 << 27, dtype=torch.int32, device=DEV)
+    lens = torch.tensor([2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    say("case: the longest")
+    out, lse = dq.int4_cache_attention(torch.from_numpy(q).to(DEV).half(), cache_of(dq, m), table, lens, return_lse=True)
+    got, many = out.double().cpu().numpy(), 18 * 2.0 ** 25 / 4096 * 2.0 ** -24
+    _, v, _ = m.read(16, small, np.array([16]), np.array([0, 16], np.int32))[0:3]
+    most = np.abs(v).max()
+    assert np.all(np.abs(got - ref) <= tol + 2.0 ** -11 * (np.abs(ref) + tol) + 2 * many * most)
+    assert np.all(np.abs(lse.cpu().numpy() - (rlse + 27 * np.log(2.0))) <= ltol + 2 * many + 2.0 ** -19)
+
+
 def test_refusals(dq):
     c = dq.Int4Cache.empty(4, 16, 2, 64, 32)
     table = torch.zeros(2, 2, dtype=torch.int32, device=DEV)
@@ -261,6 +283,13 @@ def test_refusals(dq):
     refused(dq.Int4Cache.empty, 4, 16, 2, 128, 48, match="group")
     refused(dq.Int4Cache, c.k_packed, c.k_scales, c.v_packed, c.v_scales, 64, 64, match="shape")
     refused(dq.Int4Cache, c.k_packed, c.k_scales, c.v_packed, c.v_scales, 64, 32, torch.zeros(1, device=DEV), match="both")
+    # a table without pages: no keys
+    empty = table[:, :0]
+    w(c, k, k, empty, lens)
+    assert not torch.any(torch.stack(r(c, empty, lens)))
+    for causal in (True, False):
+        out, lse = at(q + 1, c, empty, lens, causal=causal, return_lse=True)
+        assert not torch.any(out) and torch.all(torch.isneginf(lse))
     # nothing to do is no error
     none = torch.zeros(0, 2, 64, device=DEV)
     zeros = torch.zeros(3, dtype=torch.int32, device=DEV)
