@@ -87,7 +87,8 @@ struct AttentionArgs {
   int bf16;                 // q and out: 1 bfloat16, 0 binary16
   int q_wide;               // every 8 channels of q lie 16-byte aligned and head_dim is a multiple of 8
   int ratio;                // query heads per key/value head
-  float scale;
+  float scale_part;         // scale * log2 e = scale_part * 2^scale_exp, the part in [0.5, 1]
+  int scale_exp;
   int causal;
   int64_t window;           // 0: none
   void* out;

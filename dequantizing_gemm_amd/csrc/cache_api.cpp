@@ -152,8 +152,10 @@ int int4_cache_attention(const int4_cache_t* cache, const int4_cache_rows_t* row
   if (r.rows == 0 || r.batch == 0) return ok();
   if (!q || !out) return fail(INT4DQ_EINVAL, "%s: q and out must be non-NULL", fn);
   const bool wide = (uintptr_t)q % 16 == 0 && c.D % 8 == 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0;
+  int scale_exp;
+  const float scale_part = (float)frexp((double)scale * 1.44269504088896340736, &scale_exp);
   const AttentionArgs a{c, r, q, q_row_stride, q_head_stride, dtype == INT4DQ_ROWS_BF16 ? 1 : 0, wide ? 1 : 0,
-                        (int)(q_heads / c.heads), scale, causal ? 1 : 0, window, out, lse};
+                        (int)(q_heads / c.heads), scale_part, scale_exp, causal ? 1 : 0, window, out, lse};
   return hip_status(int4dq::launch_cache_attention(a, workspace, workspace_bytes, (hipStream_t)stream),
                     "int4_cache_attention launch");
 }

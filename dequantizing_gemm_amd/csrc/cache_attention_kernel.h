@@ -23,7 +23,13 @@
 // within 6 of max_j a_j + log2 max_j s'_j - 9 (log2 units), which keeps every
 // w_j below 2^15 and the large ones far above binary16's subnormals whatever
 // the values' magnitude; and it moves only when exceeded by 6, so that the
-// accumulators are rescaled a few times a sequence, not every step.
+// accumulators are rescaled a few times a sequence, not every step. Far from zero
+// (2^22) a sum of the two cannot be held: its rounding, 2^6 and more from scores of
+// 2^30 on, would end up in the exponent. There m is the largest score alone, without
+// the 6, and w_j at most a scale. For that the product of score and factor has to be
+// exact: the factor is a power of two, and the rest of scale * log2 e goes into the
+// keys' scales. (The largest score taken off every score instead: prompts 5% slower;
+// in a branch for far scores: 1 to 2%.)
 //
 // Work. A wavefront takes 64 tokens a step for 16 QT query rows; the four
 // wavefronts of a block take turns on a chunk of the tokens and are joined
@@ -328,7 +334,8 @@ struct Rows {
   int flat0, flats;                      // the first flat row, and the sequence's number of them
   int lo[QT], hi[QT];                    // visible keys
   half8_t q[QT][C];
-  float factor[QT], qsum[QT][AFF ? NG : 1];
+  float factor[QT], qsum[QT][AFF ? NG : 1];          // factor: a power of two
+  static constexpr float kFar = 0x1p22f;
   float4_t acc[QT][2 * C];               // [.][2 j]: channels of the low nibbles of byte rows 16 j .., [2 j + 1]: high
   float m[QT], l[QT], zsum[QT][AFF ? NG : 1];
   float s[QT][16];                       // scores, then probabilities: tokens token_of(0) .. token_of(15)
@@ -396,7 +403,7 @@ struct Rows {
       // most * 2^up in [2^13, 2^14)
       const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;
       const int up = most > 0.0f ? (e > 110 ? -97 : 13 - e) : 0;
-      factor[t] = __builtin_ldexpf(a.scale * 1.44269504088896340736f, -up);
+      factor[t] = __builtin_ldexpf(1.0f, a.scale_exp - up);
 #pragma unroll
       for (int g = 0; g < (AFF ? NG : 1); ++g) qsum[t][g] = 0.0f;
 #pragma unroll
@@ -422,12 +429,12 @@ struct Rows {
 
   // Scores of key tile n from its operand (a block of 32 channels each).
   template <int n>
-  __device__ __forceinline__ void score(const half8_t k[C], const StepScales<NG, AFF>& x) {
+  __device__ __forceinline__ void score(const half8_t k[C], const StepScales<NG, AFF>& x, float part) {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const float ks = half_bits_to_float((uint16_t)x.k[g]);
+        const float ks = half_bits_to_float((uint16_t)x.k[g]) * part;
         float4_t dot = {0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (AFF) {               // (8 - z) sum q
           const float z = 8.0f - (float)x.kz[g];
@@ -468,26 +475,28 @@ struct Rows {
 
   // Moves the running reference where it has to and turns the scores into
   // probabilities. The reference is the largest score plus the exponent of the
-  // largest scale: an upper bound of log2 of every weight, less 9.
+  // largest scale: an upper bound of log2 of every weight, less 9; or far from zero
+  // the largest score, an upper bound of log2 of every probability.
   __device__ __forceinline__ void settle(const uint32_t vs[NG]) {
     uint32_t big = vs[0];
 #pragma unroll
     for (int g = 1; g < NG; ++g) big = vs[g] > big ? vs[g] : big;
-    const float spread = (float)((int)(row_umax(big) >> 10) - 14 - 9);
+    const float spread = (float)((int)(row_umax(big) >> 10) - 14 - 9 - 6);
     bool move = false;
-    float cand[QT];
+    float cand[QT];                        // less 6 where it is not far
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       float top = s[t][0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, s[t][i]);
-      cand[t] = rows_max(__builtin_fmaf(top, factor[t], spread));
-      move |= cand[t] > m[t] + 6.0f;
+      top *= factor[t];
+      cand[t] = rows_max(__builtin_fabsf(top) > kFar ? top : top + spread);
+      move |= cand[t] > m[t];
     }
     if (__ballot(move) != 0) {
 #pragma unroll
       for (int t = 0; t < QT; ++t) {
-        const float to = __builtin_fmaxf(m[t], cand[t]);
+        const float to = __builtin_fmaxf(m[t], __builtin_fabsf(cand[t]) > kFar ? cand[t] : cand[t] + 6.0f);
         const float shrink = __builtin_amdgcn_exp2f(m[t] - to);
         m[t] = to;
         l[t] *= shrink;
@@ -703,7 +712,7 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
       constexpr int n = decltype(nn)::value;
       half8_t k[C];
       key_operands<C, AFF>(kw[n], k);
-      r.template score<n>(k, sc);
+      r.template score<n>(k, sc, a.scale_part);
       // no instruction, but an order: this tile's scores are finished before the
       // next one's codes are taken apart, which keeps the live registers few
 #pragma unroll
@@ -922,7 +931,7 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
       each<4>([&](auto nn) {
         constexpr int n = decltype(nn)::value;
         if constexpr (n < 3) read_keys(n + 1, k[(n + 1) & 1]);
-        r.template score<n>(k[n & 1], sc);
+        r.template score<n>(k[n & 1], sc, a.scale_part);
       });
       __builtin_amdgcn_s_setprio(0);
       read_values(0, v[0]);

@@ -1,0 +1,86 @@
+"""Attention over the 4-bit cache on MI355X where its arithmetic could leave its
+range: scores of any size below 2^96, the smallest factors, value scales that are
+far apart, hidden or negative. Bounds as in tests/test_cache_gpu.py unless a test
+derives its own."""
+import numpy as np
+import pytest
+import torch
+
+from tests.cache_model import Model, plan
+from tests.test_cache_gpu import BF16, DEV, F16, cache_of, check_attention, dev, dq, filled, rounded, say, values  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def two_level(dq, rng, D, group, affine, page, n, rows, tall, factors, dtype, scale, size=1.0):
+    """A sequence of n tokens whose keys are zero but for those in `tall`, which are
+    all the same: every score is 0 or the row's own S, from one dot product, so that
+    the softmax weighs the visible keys of the larger one alike (for |S| of 2^20 and
+    more the others are below e^(-2^20), which is 0). The last `rows` tokens are
+    queries: one vector times a power of two of either sign each. `size` multiplies the
+    values.
+
+    Bounds: each weight is rounded to binary16 (2^-11), and the exponential, the sums
+    and the division add 2^-20; the value sums round at 15 * 2^-24 of the scales for
+    each 32 tokens, and the result once to its type. lse: the score's sum of D
+    products in binary32, 2^-24 (D + 16) sum |q_d| 16 s, and 2^-22 of itself."""
+    table, pages, _ = plan(rng, [n], [rows], page)
+    m = Model(pages, page, 1, D, group, affine, fill=0x7E)
+    whole = np.array([0, n], np.int32)
+    q0 = rounded(rng.normal(size=D).astype(np.float32), dtype)
+    k = np.zeros((n, 1, D), np.float32)
+    k[sorted(tall)] = q0 * np.float32(0.25)
+    m.write(k, values(rng, n, 1, D) * np.float32(size), table, [n], whole)
+    vv = m.read(n, table, [n], whole)[1][:, 0].astype(np.float64)
+    kk, ks = (x[0].astype(np.float64) for x in m.values("k", m.page(table, 0, min(tall)), min(tall) % page))
+    vs = np.stack([m.values("v", m.page(table, 0, j), j % page)[1][0] for j in range(n)]).astype(np.float64)
+    is_tall = np.isin(np.arange(n), sorted(tall))
+    cache, table_d, lens = cache_of(dq, m), dev(table), dev(np.array([n], np.int32))
+    for turn in range(0, len(factors), min(rows, len(factors))):
+        q = (q0 * np.resize(np.roll(factors, -turn), rows)[:, None]).astype(np.float32)
+        assert np.array_equal(rounded(q, dtype), q)
+        out, lse = dq.int4_cache_attention(torch.from_numpy(q[:, None]).to(dtype).to(DEV), cache, table_d, lens,
+                                           dev(np.array([0, rows], np.int32)), scale=scale, return_lse=True)
+        torch.cuda.synchronize()
+        o, l = out[:, 0].double().cpu().numpy(), lse[:, 0].double().cpu().numpy()
+        assert np.all(np.isfinite(o)) and np.all(np.isfinite(l))
+        for i in range(rows):
+            S = scale * float(q[i].astype(np.float64) @ kk)
+            assert 2.0 ** 20 <= abs(S) < 2.0 ** 96
+            see = np.arange(n) <= n - rows + i
+            best, level = see & is_tall, S
+            if S < 0 and (see & ~is_tall).any() or not best.any():
+                best, level = see & ~is_tall, 0.0
+            ref = vv[best].mean(0)
+            tol = (2.0 ** -11 + 2.0 ** -20) * np.abs(vv[best]).mean(0) + (see.sum() / 32 + 64) * 2.0 ** -24 * 15 * vs[see].max()
+            tol = tol + torch.finfo(dtype).eps / 2 * (np.abs(ref) + tol) + (2.0 ** -25 if dtype == F16 else 0.0)
+            assert np.all(np.abs(o[i] - ref) <= tol), (i, S, np.max(np.abs(o[i] - ref) / tol))
+            want = level + np.log(best.sum())
+            ltol = scale * 2.0 ** -24 * (D + 16) * 16 * float(ks @ np.abs(q[i].astype(np.float64))) if level else 0.0
+            assert abs(l[i] - want) <= ltol + 2.0 ** -20 + 2.0 ** -22 * abs(want), (i, S, l[i], want)
+
+
+FAR = [  # D, group, affine, page, tokens, rows, tokens with the tall key, dtype, scale
+    (64, 64, False, 16, 1, 1, {0}, BF16, 0.125),
+    (128, 128, False, 16, 40, 3, {2, 9, 20}, BF16, 0.125),
+    (64, 64, True, 16, 300, 2, {7, 100, 290}, BF16, 0.125),
+    (128, 32, True, 64, 2600, 2, {3, 1000, 2590}, BF16, 0.125),              # shared out over blocks
+    (64, 64, False, 64, 9300, 1, {3, 1000, 5000, 9290}, BF16, 0.125),        # over more than 8
+    (256, 128, True, 16, 1500, 3, {1, 700, 1490}, BF16, 0.125),
+    (64, 64, False, 32, 330, 300, {40, 41, 200}, BF16, 0.125),               # the form for prompts
+    (128, 64, True, 32, 2300, 290, {2020, 2100, 2299}, BF16, 0.125),         # the same, shared out
+    (192, 192, False, 32, 330, 300, {40, 41, 200}, BF16, 0.125),
+    (64, 64, False, 16, 200, 5, {3, 77, 190}, F16, 2.0 ** 70),
+]
+
+
+@pytest.mark.parametrize("D,group,affine,page,n,rows,tall,dtype,scale", FAR)
+def test_scores_far_from_zero(dq, D, group, affine, page, n, rows, tall, dtype, scale):
+    factors = [2.0 ** 20, -2.0 ** 26, 2.0 ** 30, 2.0 ** 25, -2.0 ** 90, 2.0 ** 40, 2.0 ** 90, -2.0 ** 28, 2.0 ** 27,
+               2.0 ** 21, -2.0 ** 21, 2.0 ** 22, -2.0 ** 23, 2.0 ** 24]
+    if dtype == F16:
+        factors = [1.0, -32.0, 256.0, 4.0]
+    say("case: far", D, group, affine, page, n, rows, dtype, scale)
+    two_level(dq, np.random.default_rng(70 + n), D, group, affine, page, n, rows, tall, factors, dtype, scale)
+    if dtype == BF16:                      # value scales up to some thousands, without the room that small ones leave
+        two_level(dq, np.random.default_rng(71 + n), D, group, affine, page, n, rows, tall, factors, dtype, scale, 2.0 ** 12)
