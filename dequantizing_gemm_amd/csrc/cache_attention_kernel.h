@@ -403,7 +403,10 @@ struct Rows {
       // most * 2^up in [2^13, 2^14)
       const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;
       const int up = most > 0.0f ? (e > 110 ? -97 : 13 - e) : 0;
-      factor[t] = __builtin_ldexpf(1.0f, a.scale_exp - up);
+      // neither 0 nor infinite, which a hidden score or a score of 0 would turn to NaN: at
+      // 2^-126 and below scores, less than 2^43 here, are 0 to the last bit of their softmax
+      const int x = a.scale_exp - up;
+      factor[t] = __builtin_ldexpf(1.0f, x < -126 ? -126 : x > 127 ? 127 : x);
 #pragma unroll
       for (int g = 0; g < (AFF ? NG : 1); ++g) qsum[t][g] = 0.0f;
 #pragma unroll

@@ -84,3 +84,38 @@ def test_scores_far_from_zero(dq, D, group, affine, page, n, rows, tall, dtype, 
     two_level(dq, np.random.default_rng(70 + n), D, group, affine, page, n, rows, tall, factors, dtype, scale)
     if dtype == BF16:                      # value scales up to some thousands, without the room that small ones leave
         two_level(dq, np.random.default_rng(71 + n), D, group, affine, page, n, rows, tall, factors, dtype, scale, 2.0 ** 12)
+
+
+SMALL = [(64, 64, False, 2, [70, 1, 33], [1, 1, 1]), (128, 32, True, 2, [1300, 20], [3, 1]), (64, 64, False, 3, [230, 290], [140, 290])]
+
+
+@pytest.mark.parametrize("D,group,affine,ratio,lengths,new", SMALL)
+def test_smallest_scales(dq, D, group, affine, ratio, lengths, new):
+    """Products of scale and query down to the smallest binary32 numbers and below,
+    where all visible keys weigh the same; some are hidden in each tile."""
+    rng = np.random.default_rng(80 + D)
+    m, table, starts = filled(rng, 1, D, group, affine, 16, lengths, new)
+    q = rounded(rng.normal(size=(int(starts[-1]), ratio, D)).astype(np.float32), BF16)
+    cache = cache_of(dq, m)
+    st = None if set(new) == {1} else starts
+    for scale in (1e-45, 1e-42, 2.0 ** -126):
+        say("case: small scale", D, scale)
+        check_attention(dq, m, table, lengths, st, q, BF16, scale=scale, cache=cache)
+    tiny = rounded(q * np.float32(2.0 ** -120) * np.float32(2.0 ** -8), BF16)      # subnormal in binary32 as in bfloat16
+    assert np.any(tiny) and np.abs(tiny).max() < 2.0 ** -125
+    for scale in (2.0 ** -11, 2.0 ** -126, 1.0):
+        say("case: small queries", D, scale)
+        check_attention(dq, m, table, lengths, st, tiny, BF16, scale=scale, cache=cache)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_largest_scales(dq, rows):
+    """Products of scale and query beyond binary32, over keys that are all zero."""
+    rng = np.random.default_rng(85)
+    n = rows + 20
+    table, pages, _ = plan(rng, [n], [rows], 16)
+    m = Model(pages, 16, 1, 64, 64, False, fill=0x7E)
+    m.write(np.zeros((n, 1, 64), np.float32), values(rng, n, 1, 64), table, [n], np.array([0, n], np.int32))
+    q = rounded((rng.normal(size=(rows, 2, 64)) * 2.0 ** 96).astype(np.float32), BF16)
+    say("case: large scale", rows)
+    check_attention(dq, m, table, [n], np.array([0, rows], np.int32), q, BF16, scale=3e38)
