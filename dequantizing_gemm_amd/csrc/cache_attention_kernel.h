@@ -476,24 +476,49 @@ struct Rows {
       if (row >= have) vs[g] = 0;
   }
 
-  // Moves the running reference where it has to and turns the scores into
-  // probabilities. The reference is the largest score plus the exponent of the
-  // largest scale: an upper bound of log2 of every weight, less 9; or far from zero
-  // the largest score, an upper bound of log2 of every probability.
-  __device__ __forceinline__ void settle(const uint32_t vs[NG]) {
+  // The exponent of the largest scale of a lane's token, for reach.
+  static __device__ __forceinline__ uint32_t scale_binade(const uint32_t vs[NG]) {
     uint32_t big = vs[0];
 #pragma unroll
     for (int g = 1; g < NG; ++g) big = vs[g] > big ? vs[g] : big;
-    const float spread = (float)((int)(row_umax(big) >> 10) - 14 - 9 - 6);
-    bool move = false;
-    float cand[QT];                        // less 6 where it is not far
+    return big >> 10;
+  }
+  static __device__ __forceinline__ float binades(uint32_t e) { return (float)((int)e - 14 - 9 - 6); }
+
+  // What the reference has to reach for a lane's tokens, less 6: the largest score
+  // plus the exponent of the largest scale, an upper bound of log2 of every weight,
+  // less 9; or far from zero the largest score, an upper bound of log2 of every
+  // probability. Where tokens are hidden (each_token) each score goes with its own
+  // token's scale: one that a row does not see must not take bits from what it sees.
+  template <bool each_token>
+  __device__ __forceinline__ void reach(const uint32_t vs[NG], float cand[QT]) const {
+    const uint32_t e = scale_binade(vs);
+    const float own = binades(e), spread = binades(row_umax(e));
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       float top = s[t][0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, s[t][i]);
       top *= factor[t];
-      cand[t] = rows_max(__builtin_fabsf(top) > kFar ? top : top + spread);
+      float near = top + spread;
+      if constexpr (each_token) {
+        near = -__builtin_inff();
+        each<16>([&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          near = __builtin_fmaxf(near, s[t][i] * factor[t] + of_token<token_of(i)>(own));
+        });
+      }
+      cand[t] = __builtin_fabsf(top) > kFar ? top : near;
+    }
+  }
+
+  // Moves the running reference where it has to and turns the scores into
+  // probabilities; cand: of reach.
+  __device__ __forceinline__ void settle(float cand[QT]) {
+    bool move = false;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      cand[t] = rows_max(cand[t]);
       move |= cand[t] > m[t];
     }
     if (__ballot(move) != 0) {
@@ -732,8 +757,14 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
     uint32_t vs[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) vs[g] = sc.v[g];
-    if (masked) r.hide(step, found, work.w.keys, vs);
-    r.settle(vs);
+    float cand[QT];
+    if (masked) {
+      r.hide(step, found, work.w.keys, vs);
+      r.template reach<true>(vs, cand);
+    } else {
+      r.template reach<false>(vs, cand);
+    }
+    r.settle(cand);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       half8_t w[QT][2];
@@ -942,8 +973,14 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
       uint32_t vs[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) vs[g] = sc.v[g];
-      if (masked) r.hide(step, found, work.w.keys, vs);
-      r.settle(vs);
+      float cand[QT];
+      if (masked) {
+        r.hide(step, found, work.w.keys, vs);
+        r.template reach<true>(vs, cand);
+      } else {
+        r.template reach<false>(vs, cand);
+      }
+      r.settle(cand);
       each<NG>([&](auto gg) {
         constexpr int g = decltype(gg)::value;
         half8_t w[QT][2];

@@ -119,3 +119,43 @@ def test_largest_scales(dq, rows):
     q = rounded((rng.normal(size=(rows, 2, 64)) * 2.0 ** 96).astype(np.float32), BF16)
     say("case: large scale", rows)
     check_attention(dq, m, table, [n], np.array([0, rows], np.int32), q, BF16, scale=3e38)
+
+
+@pytest.mark.parametrize("D,group,affine,ratio,rows,dtype", [
+    (64, 64, False, 2, 14, BF16), (128, 64, True, 1, 30, F16), (128, 128, False, 2, 200, F16), (64, 32, True, 3, 140, BF16),
+    (256, 128, False, 1, 20, BF16)])
+def test_hidden_tokens_scales(dq, D, group, affine, ratio, rows, dtype):
+    """Rows before a token whose value scales are far above theirs, in the same unit of
+    16: what a row does not see takes no bits from what it sees."""
+    rng = np.random.default_rng(90 + D + rows)
+    n = rows + 20
+    for low, high, at in ((2.0 ** -13, 2.0 ** 11, n - 1), (2.0 ** -17, 2.0 ** 5, n - 2), (2.0 ** -9, 2.0 ** 13, n - rows + 5)):
+        table, pages, _ = plan(rng, [n], [rows], 16)
+        m = Model(pages, 16, 1, D, group, affine, fill=0x7E)
+        v = rng.normal(size=(n, 1, D)).astype(np.float32) * np.float32(low)
+        v[at] *= np.float32(high / low)
+        m.write(values(rng, n, 1, D), v, table, [n], np.array([0, n], np.int32))
+        q = rounded(rng.normal(size=(rows, ratio, D)).astype(np.float32), dtype)
+        say("case: hidden scales", D, rows, low, high)
+        check_attention(dq, m, table, [n], np.array([0, rows], np.int32), q, dtype)
+
+
+@pytest.mark.parametrize("D,group,affine,rows,dtype", [(64, 64, False, 1, F16), (128, 32, True, 4, BF16), (128, 128, False, 300, F16)])
+def test_any_bits_before_the_window(dq, D, group, affine, rows, dtype):
+    """Tokens before every row's window may hold any bits, negative and NaN scales of
+    either sign among them."""
+    rng = np.random.default_rng(100 + D)
+    n, window = rows + 60, 21
+    m, table, _ = filled(rng, 1, D, group, affine, 16, [n], [rows])
+    q = rounded(rng.normal(size=(rows, 2, D)).astype(np.float32), dtype)
+    starts = np.array([0, rows], np.int32)
+    for j in range(n - rows - window + 1):
+        page, slot = m.page(table, 0, j), j % 16
+        for s in "kv":
+            bits = rng.integers(0, 65536, size=m.scales[s][page, :, slot // 16, :, slot % 16].shape).astype(np.uint16)
+            m.scales[s][page, :, slot // 16, :, slot % 16] = (bits | 0x7C00 if j % 3 else bits).view(np.float16)
+            if affine:
+                m.zeros[s][page, :, slot // 16, :, slot % 16] = rng.integers(0, 256)
+    say("case: any bits", D, rows)
+    with np.errstate(invalid="ignore", over="ignore"):
+        check_attention(dq, m, table, [n], starts, q, dtype, window=window)
