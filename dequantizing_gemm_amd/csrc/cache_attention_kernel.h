@@ -476,11 +476,11 @@ struct Rows {
       if (row >= have) vs[g] = 0;
   }
 
-  // The exponent of the largest scale of a lane's token, for reach.
+  // The exponent of the largest scale of a lane's token, of either sign, for reach.
   static __device__ __forceinline__ uint32_t scale_binade(const uint32_t vs[NG]) {
-    uint32_t big = vs[0];
+    uint32_t big = vs[0] & 0x7FFFu;
 #pragma unroll
-    for (int g = 1; g < NG; ++g) big = vs[g] > big ? vs[g] : big;
+    for (int g = 1; g < NG; ++g) big = (vs[g] & 0x7FFFu) > big ? vs[g] & 0x7FFFu : big;
     return big >> 10;
   }
   static __device__ __forceinline__ float binades(uint32_t e) { return (float)((int)e - 14 - 9 - 6); }

@@ -159,3 +159,46 @@ def test_any_bits_before_the_window(dq, D, group, affine, rows, dtype):
     say("case: any bits", D, rows)
     with np.errstate(invalid="ignore", over="ignore"):
         check_attention(dq, m, table, [n], starts, q, dtype, window=window)
+
+
+@pytest.mark.parametrize("D,group,affine,lengths,new", [
+    (64, 64, False, [40, 130], [1, 1]), (128, 64, True, [70, 2100], [3, 1]), (128, 128, False, [300, 20], [290, 20]),
+    (256, 128, True, [50], [20])])
+def test_negative_scales(dq, D, group, affine, lengths, new):
+    """A cache filled elsewhere may hold a group's codes and scale both negated (the
+    distances from the zero point, with affine codes): the same values."""
+    rng = np.random.default_rng(110 + D)
+    m, table, starts = filled(rng, 2, D, group, affine, 16, lengths, new)
+    cache = cache_of(dq, m)
+    for s in "kv":
+        flip = torch.rand(m.scales[s].shape, device=DEV) < 0.5                   # [pages, heads, units, G, 16]
+        if not affine:                                                           # -8 has no opposite
+            codes = m.packed["v"] if s == "v" else np.take(m.packed["k"], np.argsort(m.key_order()), -1).reshape(
+                m.P, 2, 1, 16, -1).transpose(0, 1, 2, 4, 3)
+            eight = np.stack([(codes & 15) == 8, codes >> 4 == 8], -2).reshape(m.P, 2, 1, -1, 16)
+            any8 = np.stack([eight[..., g * m.group:(g + 1) * m.group, :].any(-2) for g in range(m.G)], -2)
+            flip &= ~dev(any8)
+        scales, packed = getattr(cache, s + "_scales"), getattr(cache, s + "_packed")
+        scales.copy_(torch.where(flip, -scales, scales))
+        channel = flip.repeat_interleave(m.group, 3)[..., :D, :]                 # [pages, heads, units, D, 16]
+        channel = torch.nn.functional.pad(channel, (0, 0, 0, 32 * m.C - D))
+        low, high = channel[..., 0::2, :], channel[..., 1::2, :]                 # of each byte
+        if s == "k":
+            order = torch.from_numpy(m.key_order()).to(DEV)
+            low, high = (x.transpose(-1, -2)[..., order].reshape(packed.shape) for x in (low, high))
+        lo, hi = packed & 15, packed >> 4
+        if affine:
+            zeros = getattr(cache, s + "_zeros")
+            zeros.copy_(torch.where(flip, 15 - zeros, zeros))
+            lo, hi = torch.where(low, 15 - lo, lo), torch.where(high, 15 - hi, hi)
+        else:
+            lo, hi = torch.where(low, (16 - lo) & 15, lo), torch.where(high, (16 - hi) & 15, hi)
+        packed.copy_(lo | hi << 4)
+    say("case: negative scales", D, group, affine)
+    whole = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    kr, vr, _ = m.read(int(whole[-1]), table, lengths, whole)
+    kg, vg = dq.int4_cache_read(cache, dev(table), dev(np.array(lengths, np.int32)), dev(whole), rows=int(whole[-1]),
+                                dtype=torch.float32)
+    assert np.array_equal(kg.cpu().numpy(), kr) and np.array_equal(vg.cpu().numpy(), vr)
+    q = rounded(rng.normal(size=(int(starts[-1]), 4, D)).astype(np.float32), BF16)
+    check_attention(dq, m, table, lengths, None if set(new) == {1} else starts, q, BF16, cache=cache)
