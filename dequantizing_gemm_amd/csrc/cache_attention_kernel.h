@@ -14,7 +14,9 @@
 // measured, the products then lose their bits below 2^-14 of a code, always
 // downward. As integers they are truncated below 2^-24 of the largest.
 //   scores: the scale multiplies the finished dot product of its group.
-//   values: w_j = p_j s'_jg is rounded to binary16 (nearest, <= 2^-11 relative);
+//   values: w_j = p_j s'_jg is rounded to binary16 (nearest: 2^-11 of w_j, or 2^-25,
+//     half a step of a subnormal, which the reference m below keeps under 2^-33 of the
+//     largest p times the largest s'; include/int4dq_cache.h states the bound);
 //     affine sums take off (z - 8) times the rounded w, so the offset cancels.
 // Queries are brought to [2^13, 2^14) by a power of two per row, which is exact
 // for bfloat16 and binary16 down to 2^-27 of the row's largest entry.

@@ -131,8 +131,13 @@ int int4_cache_read(const int4_cache_t *cache, const int4_cache_rows_t *rows, vo
  *   lse     out: dense [rows, q_heads] binary32, or NULL.
  *   Arithmetic: codes and queries are multiplied exactly and summed in
  *   binary32; probabilities and their sum are binary32; the product of a
- *   probability and a value's scale is rounded to binary16 (at most 2^-11
- *   relative) before it multiplies the value's code, summed in binary32.
+ *   probability and a value's scale is rounded to binary16 before it multiplies
+ *   the value's code, summed in binary32. That rounding is at most 2^-11 of the
+ *   product or, where this is more, 2^-33 P max(S, 2^-15) with P the largest
+ *   probability and S the largest value scale (in magnitude) of 16 tokens of a
+ *   unit that the row sees, in the unit where that is most; or 2^-25 P where the
+ *   row's largest score is 2^21 or more in magnitude. Tokens that a row does not
+ *   see have no part in this, whatever their codes, scales and zero points hold.
  *   workspace: device memory, 256-byte aligned, any contents, of at least
  *                int4_cache_attention_workspace_bytes, which lets long sequences
  *                be shared out over the whole GPU; or NULL with

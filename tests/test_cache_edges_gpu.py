@@ -202,3 +202,42 @@ def test_negative_scales(dq, D, group, affine, lengths, new):
     assert np.array_equal(kg.cpu().numpy(), kr) and np.array_equal(vg.cpu().numpy(), vr)
     q = rounded(rng.normal(size=(int(starts[-1]), 4, D)).astype(np.float32), BF16)
     check_attention(dq, m, table, lengths, None if set(new) == {1} else starts, q, BF16, cache=cache)
+
+
+@pytest.mark.parametrize("gap", [2.0 ** -20, 2.0 ** -30])
+@pytest.mark.parametrize("D,group,affine,n,rows", [(64, 64, False, 70, 1), (128, 128, True, 1500, 2), (128, 64, False, 300, 290)])
+def test_value_scales_far_apart(dq, D, group, affine, n, rows, gap):
+    """The first token of each unit of 16 takes nearly all the weight, with values far
+    below the others': each product of probability p and scale s is rounded by 2^-11 of
+    itself or by 2^-33 P max(S, 2^-15), P and S the largest among the visible tokens,
+    whichever is more, and multiplies a code up to 15. Beside that, as in the model: the
+    scores' roundings (delta, on every weight) and the sums'."""
+    rng = np.random.default_rng(120 + D)
+    table, pages, _ = plan(rng, [n], [rows], 16)
+    m = Model(pages, 16, 1, D, group, affine, fill=0x7E)
+    whole, starts = np.array([0, n], np.int32), np.array([0, rows], np.int32)
+    q0 = rng.normal(size=D).astype(np.float32)
+    k, v = rng.normal(size=(2, n, 1, D)).astype(np.float32) * np.array([1.0, 2.0 ** 14], np.float32)[:, None, None, None]
+    k[:, 0] -= np.outer(k[:, 0] @ q0, q0) / (q0 @ q0)
+    k[::16] = q0 * np.float32(50.0 * np.sqrt(D) / (q0 @ q0))       # scores of 50 against about 1
+    v[::16] *= np.float32(gap)
+    m.write(k, v, table, [n], whole)
+    q = rounded(np.repeat(q0[None, None], rows, 0), BF16)
+    say("case: far apart", D, n, rows, gap)
+    out = dq.int4_cache_attention(torch.from_numpy(q).to(BF16).to(DEV), cache_of(dq, m), dev(table), dev(np.array([n], np.int32)),
+                                  dev(starts)).double().cpu().numpy()[:, 0]
+    at = [(m.page(table, 0, j), j % 16) for j in range(n)]
+    kk, ks = (np.array([m.values("k", *x)[i][0] for x in at], np.float64) for i in (0, 1))
+    vv, vs = (np.array([m.values("v", *x)[i][0] for x in at], np.float64) for i in (0, 1))
+    for i in range(rows):
+        see, x = np.arange(n) <= n - rows + i, q[i, 0].astype(np.float64)
+        a = kk[see] @ x * D ** -0.5
+        p = np.exp(a - a.max())[:, None]
+        p /= p.sum()
+        ref = (p * vv[see]).sum(0)
+        delta = (D ** -0.5 * 2.0 ** -24 * (D + 16) * (16 * ks[see] @ np.abs(x)) + 2.0 ** -22 * np.abs(a)).max()
+        once = np.maximum(2.0 ** -11 * p * vs[see], 2.0 ** -33 * p.max() * np.maximum(vs[see].max(), 2.0 ** -15))
+        bound = 15 * (once * (vv[see] != 0)).sum(0) + (2 * delta + 2.0 ** -20) * (p * np.abs(vv[see])).sum(0)
+        bound += (see.sum() / 32 + 64) * 2.0 ** -24 * 15 * (p * vs[see]).sum(0)
+        bound += torch.finfo(BF16).eps / 2 * (np.abs(ref) + bound)
+        assert np.all(np.abs(out[i] - ref) <= bound), (i, np.max(np.abs(out[i] - ref) / bound))
