@@ -52,7 +52,9 @@ struct RowsView {
 };
 
 // Sequence and position of row t: false if no sequence owns it. For any
-// contents of starts the sequence found is inside the batch.
+// contents of starts the sequence found is inside the batch. This is the row
+// layout's definition one row at a time, for checks on the host of what the write
+// and read kernels' blocks take (StoreBlock).
 __host__ __device__ inline bool find_row(const RowsView& r, int64_t t, int* seq, int64_t* pos) {
   int b = (int)t;
   if (r.starts) {
@@ -77,6 +79,54 @@ __host__ __device__ inline int64_t find_page(const RowsView& r, const CacheView&
   const int64_t page = r.table[b * r.table_stride + (pos >> c.page_shift)];
   return page >= 0 && page < c.pages ? page : -1;
 }
+
+// ---------------------------------------------------------------- blocks of the write and read kernels
+
+// 64 positions from `base` of sequence b; its rows start at position p0 with row
+// `first` of the call, `rows` of them: slot t of the block is row first + base + t - p0
+// where that is one of them.
+struct StoreBlock {
+  int b, first, rows;
+  int64_t p0, base;
+};
+
+__host__ __device__ inline StoreBlock store_rows(const RowsView& r, int b) {
+  const int s0 = r.starts ? r.starts[b] : b, s1 = r.starts ? r.starts[b + 1] : b + 1;
+  StoreBlock x;
+  x.b = b;
+  x.first = s0 > 0 ? s0 : 0;
+  const int last = s1 < r.rows ? s1 : (int)r.rows;
+  x.rows = last > x.first ? last - x.first : 0;
+  x.p0 = (int64_t)r.lengths[b] - s1 + x.first;
+  x.base = x.p0 & ~(int64_t)63;         // positions below 0 among them
+  return x;
+}
+
+// Before sequence b come at most this many steps (n rows touch at most n / 64 + 2),
+// a number that needs no other sequence's length; the grid (store_units) has them all.
+__host__ __device__ inline int64_t steps_before(const RowsView& r, int b) {
+  const int64_t x = r.starts[b];
+  return (x < 0 ? 0 : x < r.rows ? x : r.rows) / 64 + 2 * (int64_t)b;
+}
+__host__ __device__ inline int64_t store_units(const RowsView& r) {
+  return r.starts ? r.rows / 64 + 2 * (int64_t)r.batch : r.batch;
+}
+
+// Block `unit` of the grid: false if it has no rows. search(n, x, f): the last i in
+// [0, n) with f(i) <= x (lanes.h).
+template <typename S>
+__host__ __device__ inline bool find_store_block(const RowsView& r, int unit, S search, StoreBlock* out) {
+  if (!r.starts) {
+    *out = store_rows(r, unit);
+    return true;
+  }
+  const int b = search(r.batch, unit, [&](int i) { return steps_before(r, i); });
+  *out = store_rows(r, b);
+  out->base += (unit - steps_before(r, b)) * 64;
+  return out->base >= out->p0 - 63 && out->base < out->p0 + out->rows;
+}
+
+// ---------------------------------------------------------------- attention
 
 // Arguments of the attention kernels.
 struct AttentionArgs {

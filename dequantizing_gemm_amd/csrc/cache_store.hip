@@ -41,45 +41,6 @@ struct RowArray {
   int wide;                  // 8 channels lie 16-byte aligned (binary32: 32 bytes from a 16-byte boundary)
 };
 
-// ---------------------------------------------------------------- the block's share
-
-// 64 positions from `base` of sequence b; its rows start at position p0 with row
-// `first` of the call, `rows` of them.
-struct StoreBlock {
-  int b, first, rows;
-  int64_t p0, base;
-};
-
-__device__ __forceinline__ StoreBlock store_rows(const RowsView& r, int b) {
-  const int s0 = r.starts ? r.starts[b] : b, s1 = r.starts ? r.starts[b + 1] : b + 1;
-  StoreBlock x;
-  x.b = b;
-  x.first = s0 > 0 ? s0 : 0;
-  const int last = s1 < r.rows ? s1 : (int)r.rows;
-  x.rows = last > x.first ? last - x.first : 0;
-  x.p0 = (int64_t)r.lengths[b] - s1 + x.first;
-  x.base = (x.p0 >> 6) << 6;
-  return x;
-}
-
-// Before sequence b come at most this many steps (n rows touch at most n / 64 + 2),
-// a number that needs no other sequence's length; the grid has them all.
-__device__ __forceinline__ int64_t steps_before(const RowsView& r, int b) {
-  const int64_t x = r.starts[b];
-  return (x < 0 ? 0 : x < r.rows ? x : r.rows) / 64 + 2 * (int64_t)b;
-}
-
-__device__ __forceinline__ bool find_store_block(const RowsView& r, int unit, StoreBlock* out) {
-  if (!r.starts) {
-    *out = store_rows(r, unit);
-    return true;
-  }
-  const int b = lane_search(r.batch, unit, [&](int i) { return steps_before(r, i); });
-  *out = store_rows(r, b);
-  out->base += (unit - steps_before(r, b)) * 64;
-  return out->base >= out->p0 - 63 && out->base < out->p0 + out->rows;
-}
-
 // ---------------------------------------------------------------- elements
 
 template <int DT>
@@ -248,7 +209,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheView c, RowsView 
   __shared__ int64_t units[4];
   __shared__ uint32_t written[4];                    // a bit for each token of the unit
   StoreBlock w;
-  if (!find_store_block(r, blockIdx.x, &w)) return;
+  if (!find_store_block(r, blockIdx.x, LaneSearch{}, &w)) return;
   find_units(c, r, w, units);
   const int tid = threadIdx.x, token = tid >> 2, a = tid & 3, ts = token & 15;
   const int64_t at_row = w.base + token - w.p0, unit0 = units[token >> 4];       // a wavefront is a unit
@@ -307,7 +268,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(CacheView c, RowsView r
                                                          int heads_per_block) {
   constexpr int DB = 16 * C;
   StoreBlock w;
-  if (!find_store_block(r, blockIdx.x, &w)) return;
+  if (!find_store_block(r, blockIdx.x, LaneSearch{}, &w)) return;
   const int tid = threadIdx.x, slots = (1 << c.page_shift) - 1;
   const int head0 = blockIdx.y * heads_per_block;
   const int head1 = head0 + heads_per_block < c.heads ? head0 + heads_per_block : c.heads;
@@ -397,7 +358,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(CacheView c, RowsView r
 template <int DT, int C>
 void launch_store(bool write, const CacheView& c, const RowsView& r, const RowArray& k, const RowArray& v,
                   hipStream_t stream) {
-  const int64_t units = r.starts ? r.rows / 64 + 2 * (int64_t)r.batch : r.batch;
+  const int64_t units = store_units(r);
   const dim3 block(256);
   if (write) {
     const dim3 grid((unsigned)units, (unsigned)c.heads, 2);

@@ -1,4 +1,5 @@
-// lanes.h -- sums over a wavefront's lanes, and a search by all of them.
+// lanes.h -- sums over a wavefront's lanes, and a search by all of them (whose steps
+// are host code too, for checks without a GPU).
 #pragma once
 
 #include <type_traits>
@@ -40,21 +41,34 @@ __device__ __forceinline__ int lane_max(int v) {
   return __builtin_amdgcn_readfirstlane(v);
 }
 
-// The last i in [0, n) with f(i) <= x, where f does not decrease; 0 if there is
-// none, and some i in range whatever f does. The lanes try 64 places at a time, so
-// that up to 64 take one load and 4096 two.
-template <typename F>
-__device__ __forceinline__ int lane_search(int n, int64_t x, F f) {
-  const int lane = threadIdx.x & (kWave - 1);
+// A search by 64 lanes, 64 places at a time, so that up to 64 take one load and 4096
+// two. below(from, apart, n): a bit for each lane l with l * apart < n and place
+// from + l * apart at or below what is searched for.
+template <typename B>
+__host__ __device__ __forceinline__ int search_by_lanes(int n, B below) {
   int from = 0;
   while (n > 1) {
     const int apart = (n + kWave - 1) / kWave;
-    const uint64_t below = __ballot(lane * apart < n && f(from + lane * apart) <= x);
-    const int at = below ? 63 - __builtin_clzll(below) : 0;
+    const uint64_t bits = below(from, apart, n);
+    const int at = bits ? 63 - __builtin_clzll(bits) : 0;
     from += at * apart;
     n = n - at * apart < apart ? n - at * apart : apart;
   }
   return from;
 }
+
+// The last i in [0, n) with f(i) <= x, where f does not decrease; 0 if there is
+// none, and some i in range whatever f does.
+template <typename F>
+__device__ __forceinline__ int lane_search(int n, int64_t x, F f) {
+  const int lane = threadIdx.x & (kWave - 1);
+  return search_by_lanes(n, [&](int from, int apart, int left) -> uint64_t {
+    return __ballot(lane * apart < left && f(from + lane * apart) <= x);
+  });
+}
+struct LaneSearch {
+  template <typename F>
+  __device__ __forceinline__ int operator()(int n, int64_t x, F f) const { return lane_search(n, x, f); }
+};
 
 }  // namespace int4dq
