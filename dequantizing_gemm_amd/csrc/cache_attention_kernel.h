@@ -16,7 +16,9 @@
 //   scores: the scale multiplies the finished dot product of its group.
 //   values: w_j = p_j s'_jg is rounded to binary16 (nearest: 2^-11 of w_j, or 2^-25,
 //     half a step of a subnormal, which the reference m below keeps under 2^-33 of the
-//     largest p times the largest s'; include/int4dq_cache.h states the bound);
+//     largest p times the largest s'; include/int4dq_cache.h states the bound), since
+//     the matrix instructions take no wider operand beside binary16 codes, and a second
+//     product for the remainder would double the values' matrix work;
 //     affine sums take off (z - 8) times the rounded w, so the offset cancels.
 // Queries are brought to [2^13, 2^14) by a power of two per row, which is exact
 // for bfloat16 and binary16 down to 2^-27 of the row's largest entry.
@@ -50,7 +52,7 @@
 // generation, 64 sequences of 130 to 8190 tokens, groups of 64, bfloat16: memory, 295
 // MB in 67 us. One sequence of 131071 tokens, groups of 32 with zero points: the
 // VALU, which takes codes apart and applies scales; 159 MB in 50 us. A prompt of
-// 4096 tokens: 137 GFLOP in 188 us, the VALU busy for 56% of it and the matrix pipes
+// 4096 tokens: 137 GFLOP in 192 us, the VALU busy for 56% of it and the matrix pipes
 // for 28%, with little overlap at two wavefronts a SIMD.
 #pragma once
 

@@ -10,7 +10,7 @@
 // with more tiles than that, tiles are cut down to the average share; and with a
 // few more, which would leave most of the GPU idle for their length, all are cut
 // further, to at most 3 target blocks (4 prompts in chunks, 149 tiles and a target of
-// 128: 253 us uncut, 234 so).
+// 128: 260 us uncut, 237 so).
 // So cuts add at most `target` blocks, and a tile of c > 1 chunks adds
 // c - 1 >= c / 2 of them, or the blocks are at most 3 target: that bounds the grid
 // and the number of partial results, which the host has to know.
@@ -34,8 +34,9 @@ struct Schedule {
 };
 
 // From more sequences than a wavefront looks through at once, their blocks are
-// counted once for all, by a kernel before the attention kernel (1024 sequences of 512
-// tokens: 185 us; looked through by every block, 402 us; 256 of them: 51 and 63).
+// counted once for all, by a kernel before the attention kernel (when that came in, 1024
+// sequences of 512 tokens: 185 us; looked through by every block, 402 us; 256 of them:
+// 51 and 63; 1024 of them take 129 us now).
 constexpr int kScanBatch = 64;
 
 // The first token of the 16-token unit u of a step. Unsigned: loads run a few steps
@@ -211,7 +212,8 @@ inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   s.target = (resident * kComputeUnits + c.heads - 1) / c.heads;
   // Four for each wavefront of the form for few rows (16 sequences of 2650 tokens, 3 to
   // 6 rows each, with at least one each: 40 us, four: 35; one row of 2000 tokens 18.7
-  // and 17.7).
+  // and 17.7). The form for prompts, whose wavefronts all take every step, has the same
+  // number; another was not measured for it.
   s.min_steps = 16;
   // Where no sequence can have more, every tile is left to one block and the join
   // kernel's launch is saved.

@@ -6,7 +6,7 @@
 // is bound by memory (4 sequences of 9001 to 40961 tokens, 8 heads of 128, to
 // bfloat16: 679 MB in 186 us, 3.7 TB/s), writing by the rounding's instructions (12
 // prompts of 300 to 4100 tokens, 8 heads of 128, groups of 32 with zero points, from
-// bfloat16: 57 us, the VALU busy for 73% of it), one token of one sequence by the
+// bfloat16: 58 us, the VALU busy for 74% of it), one token of one sequence by the
 // chain of dependent loads (5 us either way).
 //
 // Work decomposition: a block of 256 threads takes 64 positions (a step: four of
@@ -19,9 +19,10 @@
 // are the thread's own and a DPP butterfly over the token's four threads. Value
 // codes, whose bytes lie a token apart, go through LDS and leave as 16-byte rows of
 // a unit; a unit of which some tokens are not written (a run's ragged ends) leaves
-// byte by byte. Reading back, a thread takes 8 channels of a token's keys, or one
-// 16-token byte row of the values (two channels of 16 tokens), so that a
-// wavefront's stores cover whole rows.
+// byte by byte. Reading back, a thread takes 8 channels of a token's keys, so that a
+// wavefront's store is 64 bytes (of two-byte elements) in each of 16 rows, or one
+// 16-token byte row of the values (two channels of 16 tokens), whose stores cover
+// whole rows.
 #include <type_traits>
 
 #include "cache.h"

@@ -25,7 +25,8 @@
  *   v_packed [pages, heads, page_size / 16, DB, 16]: channel d of token t is
  *            nibble d % 2 of byte [t / 16, d / 2, t % 16].
  *   k_scales, v_scales [pages, heads, page_size / 16, G, 16] binary16, the
- *            scale of group g of token t at [t / 16, g, t % 16].
+ *            scale of group g of token t at [t / 16, g, t % 16] (written ones are
+ *            not negative; a cache filled elsewhere may hold either sign).
  *   k_zeros, v_zeros   bytes of the same shape, or both NULL (symmetric codes).
  * k_packed, v_packed, the scales and the zeros are 16-byte aligned.
  *
@@ -129,7 +130,8 @@ int int4_cache_read(const int4_cache_t *cache, const int4_cache_rows_t *rows, vo
  *                elements apart, channels side by side.
  *   out     out: dense [rows, q_heads, head_dim] of `dtype`.
  *   lse     out: dense [rows, q_heads] binary32, or NULL.
- *   Arithmetic: codes and queries are multiplied exactly and summed in
+ *   Arithmetic: codes and queries are multiplied exactly (queries below 2^-27 of
+ *   their row's largest as rounded to 2^-38 of it) and summed in
  *   binary32; probabilities and their sum are binary32; the product of a
  *   probability and a value's scale is rounded to binary16 before it multiplies
  *   the value's code, summed in binary32. That rounding is at most 2^-11 of the
@@ -144,6 +146,10 @@ int int4_cache_read(const int4_cache_t *cache, const int4_cache_rows_t *rows, vo
  *                workspace_bytes = 0, and any smaller size runs without that or
  *                with less of it.
  *                Calls that share a workspace must not overlap.
+ *   Speed: prompts take about twice as long with heads of more than 192 channels in
+ *   groups of 32 (with zero points, of 64 too), and with heads of 129 to 192 channels
+ *   and zero points in groups of 32 or 128; groups of 128 of 192 channels, and of 64 of
+ *   96, cost what groups of 32 do.
  * Preconditions not checked: q is finite and below 2^100 in magnitude, and so are
  * the scores a_j below 2^96.
  * Errors: those of int4_cache_write, and EINVAL for q_heads that is no multiple
