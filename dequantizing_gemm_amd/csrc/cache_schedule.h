@@ -212,8 +212,10 @@ inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   s.target = (resident * kComputeUnits + c.heads - 1) / c.heads;
   // Four for each wavefront of the form for few rows (16 sequences of 2650 tokens, 3 to
   // 6 rows each, with at least one each: 40 us, four: 35; one row of 2000 tokens 18.7
-  // and 17.7). The form for prompts, whose wavefronts all take every step, has the same
-  // number; another was not measured for it.
+  // and 17.7). The form for prompts has the same number, though its wavefronts all take
+  // every step: that suits many rows (8 sequences, 512 rows each: 87 us with 16, 10 and
+  // 6) better than few on one sequence (400 rows on 3000 tokens 47, 37 and 35 us; 1200
+  // rows on 1500 tokens 41, 36 and 40).
   s.min_steps = 16;
   // Where no sequence can have more, every tile is left to one block and the join
   // kernel's launch is saved.
