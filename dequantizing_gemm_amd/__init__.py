@@ -40,7 +40,8 @@ __all__ = ["quantize_int4", "quantize_int4_affine", "unpack_int4", "dequantize_i
            "matmul_select",
            "num_groups", "packed_bytes", "lib", "LIB_PATH", "Int4Error", "PATHS",
            "Int4Cache", "int4_cache_write", "int4_cache_read", "int4_cache_attention",
-           "cache_attention_workspace_bytes", "cache_attention_workspace"]
+           "cache_attention_workspace_bytes", "cache_attention_workspace",
+           "int4_cache_release", "int4_cache_extend", "int4_cache_append"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libint4dq.so")
 
@@ -347,3 +348,4 @@ def matmul_select(x, packed, scales, K, group=128) -> str:
 
 from .cache import (Int4Cache, cache_attention_workspace, cache_attention_workspace_bytes,  # noqa: E402
                     int4_cache_attention, int4_cache_read, int4_cache_write)
+from .cache_step import int4_cache_append, int4_cache_extend, int4_cache_release  # noqa: E402
