@@ -252,33 +252,37 @@ def int4_cache_read(cache: Int4Cache, page_table: torch.Tensor, lengths: torch.T
     return out
 
 
-def _workspace_bytes(cache, plan, q_heads):
-    n = lib.int4_cache_attention_workspace_bytes(cache._ref, ctypes.addressof(plan), q_heads)
+def _workspace_bytes(cache, plan, q_heads, shares=False):
+    if shares:
+        n = lib.int4_cache_attention_ex_workspace_bytes(cache._ref, ctypes.addressof(plan), q_heads, 1)
+    else:
+        n = lib.int4_cache_attention_workspace_bytes(cache._ref, ctypes.addressof(plan), q_heads)
     if n < 0:
         raise ValueError(lib.int4_last_error().decode())
     return n
 
 
-def cache_attention_workspace_bytes(cache: Int4Cache, batch: int, rows: int, q_heads: int) -> int:
+def cache_attention_workspace_bytes(cache: Int4Cache, batch: int, rows: int, q_heads: int, shared: bool = False) -> int:
     """Bytes of workspace int4_cache_attention uses for these sizes: ``rows`` rows
     of ``q_heads`` query heads over ``batch`` sequences, whatever their page tables
-    (a call whose table is short takes less, or none)."""
+    (a call whose table is short takes less, or none); with ``shared`` of calls that
+    are given shared tokens too."""
     _is_cache(cache)
     one = None if rows == batch else 1
     most = 2 ** 31 - 1
-    return _workspace_bytes(cache, _RowsStruct(None, most, most, None, one, batch, rows), q_heads)
+    return _workspace_bytes(cache, _RowsStruct(None, most, most, None, one, batch, rows), q_heads, shared)
 
 
-def cache_attention_workspace(cache: Int4Cache, batch: int, rows: int, q_heads: int) -> torch.Tensor:
+def cache_attention_workspace(cache: Int4Cache, batch: int, rows: int, q_heads: int, shared: bool = False) -> torch.Tensor:
     """A workspace tensor for int4_cache_attention(..., workspace=)."""
-    return torch.empty(cache_attention_workspace_bytes(cache, batch, rows, q_heads), dtype=torch.uint8,
+    return torch.empty(cache_attention_workspace_bytes(cache, batch, rows, q_heads, shared), dtype=torch.uint8,
                        device=cache.device)
 
 
 def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Tensor, lengths: torch.Tensor,
                          starts: torch.Tensor | None = None, *, scale: float | None = None, causal: bool = True,
                          window: int = 0, return_lse: bool = False, out: torch.Tensor | None = None,
-                         workspace: torch.Tensor | None = None):
+                         workspace: torch.Tensor | None = None, sinks: int = 0, shared: torch.Tensor | None = None):
     """Softmax attention of q [rows, q_heads, head_dim] (float16 or bfloat16, any
     row and head strides) over the cache: out of q's shape and dtype, and with
     ``return_lse`` the logarithm of each softmax sum, float32 [rows, q_heads].
@@ -289,7 +293,12 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
     row that sees none gets 0 and an lse of -infinity. ``scale`` multiplies the
     scores (default head_dim ** -0.5). ``workspace``: a uint8 tensor from
     cache_attention_workspace; without one the call takes its scratch from
-    torch's allocator."""
+    torch's allocator.
+
+    ``sinks``: with a window, the first ``sinks`` tokens stay visible too. ``shared``
+    int32 [1] on the GPU: all sequences begin with the same shared[0] tokens, which
+    are then read once for many sequences with few rows each, through the first row
+    of ``page_table``; the result is what it is without."""
     _is_cache(cache)
     q_heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
     qs = _rows_array(cache, q, "q", q_heads)
@@ -306,8 +315,12 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
         if tuple(out.shape) != tuple(q.shape) or out.device != q.device:
             raise ValueError(f"out must be {tuple(q.shape)} on {q.device}")
     lse = torch.empty((rows, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
+    if shared is not None:
+        _int32(cache, "shared", shared, 1)
+        if shared.shape[0] != 1:
+            raise ValueError(f"shared must have one entry (got {shared.shape[0]})")
     if workspace is None:
-        n = _workspace_bytes(cache, plan, q_heads)
+        n = _workspace_bytes(cache, plan, q_heads, shared is not None)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     else:
@@ -315,7 +328,12 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
         if workspace.device != q.device:
             raise ValueError(f"workspace must be on {q.device}")
         n = workspace.numel()
-    _call(cache, lib.int4_cache_attention, "int4_cache_attention", ctypes.addressof(plan), q.data_ptr(), *qs,
-          ROWS_DTYPES[q.dtype], q_heads, cache.head_dim ** -0.5 if scale is None else scale, bool(causal), int(window),
-          out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr() if n else None, n)
+    args = (ctypes.addressof(plan), q.data_ptr(), *qs, ROWS_DTYPES[q.dtype], q_heads,
+            cache.head_dim ** -0.5 if scale is None else scale, bool(causal), int(window))
+    to = (out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr() if n else None, n)
+    if sinks or shared is not None:
+        _call(cache, lib.int4_cache_attention_ex, "int4_cache_attention", *args, int(sinks),
+              None if shared is None else shared.data_ptr(), *to)
+    else:
+        _call(cache, lib.int4_cache_attention, "int4_cache_attention", *args, *to)
     return (out, lse) if return_lse else out

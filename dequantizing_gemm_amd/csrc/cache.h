@@ -143,7 +143,15 @@ struct AttentionArgs {
   int64_t window;           // 0: none
   void* out;
   float* lse;               // or nullptr
+  int64_t sinks;            // with a window: the first tokens that stay visible
+  // A batch whose sequences begin with the same tokens is computed in two parts
+  // whose partial results are joined: the shared tokens, for the rows of all sequences
+  // as one, and each sequence's own tokens behind them.
+  int part;                 // kWhole, kOwnPart or kSharedPart
+  const int32_t* shared;    // the number of shared tokens (parts)
+  int all;                  // kSharedPart: the sequences of the batch; r.batch is 1
 };
+constexpr int kWhole = 0, kOwnPart = 1, kSharedPart = 2;
 
 hipError_t launch_cache_write(const CacheView& c, const RowsView& r, const void* k, int64_t k_row_stride,
                               int64_t k_head_stride, const void* v, int64_t v_row_stride,

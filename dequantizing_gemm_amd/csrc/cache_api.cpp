@@ -3,7 +3,6 @@
 // made before the arguments have been validated.
 #include <hip/hip_runtime.h>
 
-#include <math.h>
 #include <stdint.h>
 
 #include "../../include/int4dq_cache.h"
@@ -19,6 +18,7 @@ using int4dq::hip_status;
 using int4dq::ok;
 
 using int4dq::call_fits;
+using int4dq::check_attention;
 using int4dq::check_cache;
 using int4dq::ll;
 using int4dq::strides_ok;
@@ -66,33 +66,11 @@ int int4_cache_read(const int4_cache_t* cache, const int4_cache_rows_t* rows, vo
 int int4_cache_attention(const int4_cache_t* cache, const int4_cache_rows_t* rows, const void* q, int64_t q_row_stride,
                          int64_t q_head_stride, int dtype, int64_t q_heads, float scale, int causal, int64_t window,
                          void* out, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
-  const char* fn = "int4_cache_attention";
-  CacheView c;
-  RowsView r;
-  const int rc = check_cache(fn, cache, rows, true, &c, &r);
+  AttentionArgs a;
+  const int rc = check_attention("int4_cache_attention", cache, rows, q, q_row_stride, q_head_stride, dtype, q_heads, scale,
+                                 causal, window, out, lse, workspace, workspace_bytes, &a);
   if (rc != INT4DQ_OK) return rc;
-  if (dtype != INT4DQ_ROWS_F16 && dtype != INT4DQ_ROWS_BF16)
-    return fail(INT4DQ_EINVAL, "%s: dtype must be binary16 or bfloat16 (got %d)", fn, dtype);
-  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads)
-    return fail(INT4DQ_EINVAL, "%s: q_heads must be a multiple of heads, up to 65535 (got %lld, %d)", fn, (ll)q_heads, c.heads);
-  if (!call_fits(r, c, q_heads))
-    return fail(INT4DQ_EINVAL, "%s: rows * q_heads must be up to 2^27 and batch * heads up to 2^22", fn);
-  if (!isfinite(scale) || !(scale > 0.0f))
-    return fail(INT4DQ_EINVAL, "%s: scale must be finite and above 0 (got %g)", fn, (double)scale);
-  if (window < 0 || (window > 0 && !causal))
-    return fail(INT4DQ_EINVAL, "%s: window must be >= 0, and needs causal (got %lld)", fn, (ll)window);
-  if (!strides_ok(q_row_stride, q_head_stride))
-    return fail(INT4DQ_EINVAL, "%s: a stride is out of range", fn);
-  if (workspace_bytes < 0 || (workspace_bytes > 0 && !workspace))
-    return fail(INT4DQ_EINVAL, "%s: workspace_bytes must be >= 0, with a non-NULL workspace when > 0", fn);
-  if ((uintptr_t)workspace % 256) return fail(INT4DQ_EINVAL, "%s: workspace must be 256-byte aligned", fn);
-  if (r.rows == 0 || r.batch == 0) return ok();
-  if (!q || !out) return fail(INT4DQ_EINVAL, "%s: q and out must be non-NULL", fn);
-  const bool wide = (uintptr_t)q % 16 == 0 && c.D % 8 == 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0;
-  int scale_exp;
-  const float scale_part = (float)frexp((double)scale * 1.44269504088896340736, &scale_exp);
-  const AttentionArgs a{c, r, q, q_row_stride, q_head_stride, dtype == INT4DQ_ROWS_BF16 ? 1 : 0, wide ? 1 : 0,
-                        (int)(q_heads / c.heads), scale_part, scale_exp, causal ? 1 : 0, window, out, lse};
+  if (a.r.rows == 0 || a.r.batch == 0) return ok();
   return hip_status(int4dq::launch_cache_attention(a, workspace, workspace_bytes, (hipStream_t)stream),
                     "int4_cache_attention launch");
 }

@@ -63,7 +63,7 @@ __global__ __launch_bounds__(1024) void cache_attention_plan_kernel(AttentionArg
       const SequenceWork w = of(b);
       const int chunks = w.tiles > 0 ? chunks_of(w.steps, per) : 0;
       mine = chunks * w.tiles;
-      mine_slots = chunks > 1 ? mine : 0;
+      mine_slots = chunks > 1 || sched.partial ? mine : 0;
     }
     int upto = lane_scan(mine), slots_upto = lane_scan(mine_slots);
     if (lane == kWave - 1) sums[turn][wave] = PlanEntry{upto, slots_upto};
@@ -170,10 +170,20 @@ __global__ __launch_bounds__(256) void cache_attention_join_kernel(AttentionArgs
   }
 }
 
+}  // namespace
+
+hipError_t launch_cache_attention_plan(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream) {
+  hipLaunchKernelGGL(cache_attention_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s, ws);
+  return hipGetLastError();
+}
+
+namespace {
+
 template <int C>
 hipError_t launch_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream) {
-  if (s.planned) hipLaunchKernelGGL(cache_attention_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s, ws);
-  hipError_t e = launch_attention_width<C>(a, s, ws, stream);
+  hipError_t e = s.planned ? launch_cache_attention_plan(a, s, ws, stream) : hipSuccess;
+  if (e == hipSuccess)
+    e = sink_end(a) > 0 ? launch_attention_width<C, true>(a, s, ws, stream) : launch_attention_width<C, false>(a, s, ws, stream);
   if (e != hipSuccess || s.target == 0) return e;
   const unsigned rows = (unsigned)(a.r.starts || a.ratio > 4 ? 4 : a.ratio);
   hipLaunchKernelGGL(cache_attention_join_kernel<C>, dim3((unsigned)(workspace_slots(s) * a.c.heads), rows), dim3(256),
@@ -183,11 +193,26 @@ hipError_t launch_width(const AttentionArgs& a, const Schedule& s, const Workspa
 
 }  // namespace
 
-extern template hipError_t launch_attention_width<2>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
-extern template hipError_t launch_attention_width<3>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
-extern template hipError_t launch_attention_width<4>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
-extern template hipError_t launch_attention_width<6>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
-extern template hipError_t launch_attention_width<8>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
+extern template hipError_t launch_attention_width<2, false>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<2, true>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<3, false>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<3, true>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<4, false>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<4, true>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<6, false>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<6, true>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<8, false>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
+extern template hipError_t launch_attention_width<8, true>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                           hipStream_t);
 
 int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int ratio) {
   const Schedule s = plan_of(c, r, ratio);

@@ -111,7 +111,7 @@ __device__ __forceinline__ bool find_block(const AttentionArgs& a, const Schedul
       return lane_value(lane_scan(w.tiles > 0 ? (chunks_of(w.steps, x) - 1) * w.tiles : 0), kWave - 1);
     });
     const int chunks = w.tiles > 0 ? chunks_of(w.steps, per) : 0;
-    const int mine = chunks * w.tiles, mine_slots = chunks > 1 ? mine : 0;
+    const int mine = chunks * w.tiles, mine_slots = chunks > 1 || s.partial ? mine : 0;
     const int upto = lane_scan(mine), slots_upto = lane_scan(mine_slots);
     *used = lane_value(slots_upto, kWave - 1);
     const uint64_t hit = __ballot(unit >= upto - mine && unit < upto);
@@ -462,17 +462,34 @@ struct Rows {
     }
   }
 
-  // Hides the step's tokens that a row does not see. Scales of tokens that the
-  // sequence does not have (their memory may hold anything) become 0.
-  __device__ __forceinline__ void hide(int step, uint32_t found, int keys, uint32_t vs[NG]) {
+  // Hides the step's tokens that a row does not see: all but [lo, hi) and (MORE), below
+  // hi, the first tokens [first, sinks). Scales of tokens that the sequence does not have
+  // (their memory may hold anything) become 0.
+  template <bool MORE>
+  __device__ __forceinline__ void hide(int step, uint32_t found, int keys, int first, int sinks, uint32_t vs[NG]) {
     const int token0 = step * kStep + 16 * quarter;
     const bool there = (found >> quarter) & 1u;
+    if constexpr (MORE) {
+      auto below = [&](int token) {      // a bit for each token of the unit before this one
+        const int n = token - token0;
+        return (1u << (n < 0 ? 0 : n < 16 ? n : 16)) - 1u;
+      };
+      const uint32_t kept = below(sinks) & ~below(first);
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      const int from = lo[t] - token0, to = there ? hi[t] - token0 : -1;
+      for (int t = 0; t < QT; ++t) {
+        const uint32_t sees = there ? below(hi[t]) & (~below(lo[t]) | kept) : 0u;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (token_of(i) < from || token_of(i) >= to) s[t][i] = -__builtin_inff();
+        for (int i = 0; i < 16; ++i)
+          if (!(sees & (1u << token_of(i)))) s[t][i] = -__builtin_inff();
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        const int from = lo[t] - token0, to = there ? hi[t] - token0 : -1;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (token_of(i) < from || token_of(i) >= to) s[t][i] = -__builtin_inff();
+      }
     }
     const int have = there ? keys - token0 : 0;
 #pragma unroll
@@ -658,7 +675,7 @@ __device__ __forceinline__ bool begin_block(const AttentionArgs& a, const Schedu
   const bool found = find_block(a, sched, ws, blockIdx.x / heads, work, &used);
   if (sched.target > 0 && !sched.planned && blockIdx.x == 0 && threadIdx.x == 0) *ws.used = used;
   if (!found) return false;
-  if (work->chunks > 1 && blockIdx.x % heads == 0 && threadIdx.x == 0)
+  if ((work->chunks > 1 || sched.partial) && blockIdx.x % heads == 0 && threadIdx.x == 0)
     ws.record[work->slot] = PartRecord{work->w.first, work->tile * sched.tile_rows, work->w.rows * a.ratio, work->chunk,
                                        work->chunks, {}};
   return true;
@@ -670,21 +687,57 @@ struct Span {
   int lo_first, hi_first, lo_last, hi_last;
   __device__ __forceinline__ Span(const AttentionArgs& a, const SequenceWork& w, int flat0, int n) {
     const int flats = w.rows * a.ratio;
+    if (a.part == kSharedPart) {         // rows of many sequences, in no order: the least and the largest
+      const int t0 = (uint32_t)flat0 / (uint32_t)a.ratio;
+      const int t1 = (uint32_t)((flat0 + n < flats ? flat0 + n : flats) - 1) / (uint32_t)a.ratio;
+      int least[2] = {INT32_MAX, INT32_MAX}, most[2] = {0, 0};
+      for (int t = t0 + (threadIdx.x & (kWave - 1)); t <= t1; t += kWave) {
+        int lo, hi;
+        visible(a, w, t, &lo, &hi);
+        if (hi > lo) least[0] = lo < least[0] ? lo : least[0];
+        else if (sink_end(a) == 0) lo = hi = 0;      // a row that sees nothing adds no steps
+        least[1] = hi < least[1] ? hi : least[1];
+        most[0] = lo > most[0] ? lo : most[0];
+        most[1] = hi > most[1] ? hi : most[1];
+      }
+      lo_last = lane_max(most[0]);
+      hi_last = lane_max(most[1]);
+      hi_first = INT32_MAX - lane_max(INT32_MAX - least[1]);
+      lo_first = INT32_MAX - lane_max(INT32_MAX - least[0]);
+      if (lo_first > hi_last) lo_first = hi_last;
+      return;
+    }
     visible(a, w, (uint32_t)flat0 / (uint32_t)a.ratio, &lo_first, &hi_first);
     visible(a, w, (uint32_t)((flat0 + n < flats ? flat0 + n : flats) - 1) / (uint32_t)a.ratio, &lo_last, &hi_last);
   }
   __device__ __forceinline__ bool masks(int step) const { return step_masked(step, lo_last, hi_first); }
 };
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The kernels come in two forms: MORE also takes first tokens that stay visible and the
+// parts of a batch that shares tokens. What other calls run has none of that in it: as
+// one form the registers of both would not do (up to 10 more, and spills where tiles
+// fill them).
+template <bool MORE>
+__device__ __forceinline__ void only_whole(AttentionArgs* a, Schedule* s) {
+  if constexpr (!MORE) {
+    a->sinks = 0;
+    a->part = kWhole;
+    s->partial = 0;
+  }
+}
+
 // ---------------------------------------------------------------- few rows
 
 // C blocks of 32 channels, GC of them to a scale (scale_blocks), QT tiles of 16
 // query rows. The block's four wavefronts take turns on the steps; their results
 // are joined through LDS.
-template <int C, int GC, int QT, bool AFF>
+template <int C, int GC, int QT, bool AFF, bool MORE>
 __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void cache_attention_kernel(
     AttentionArgs a, Schedule sched, Workspace ws) {
   constexpr int NG = C / GC, DB = 16 * C, TR = 16 * QT;
+  only_whole<MORE>(&a, &sched);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
   const int heads = a.c.heads, kh = blockIdx.x % heads;
@@ -696,8 +749,8 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
   r.flat0 = work.tile * TR;
   r.flats = work.w.rows * a.ratio;
   const Span span(a, work.w, r.flat0, TR);
-  int begin, end;
-  chunk_steps(span.lo_first, span.hi_last, work.chunk, work.chunks, &begin, &end);
+  const TileSteps<MORE> steps = tile_steps<MORE>(a, span.lo_first, span.hi_last, work.chunk, work.chunks).uniform();
+  const int first = uniform(first_key(a)), sinks = uniform(sink_end(a)), end = steps.end;
   Words<4> raw[QT][C];
   r.load(a, work.w, kh, raw);
 
@@ -721,25 +774,26 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
     for (int j = 0; j < C; ++j) vw[j] = load_words<4>(p + j * 256);
     load_value_scales(a.c, vu, r.row, r.group_of, &sc);
   };
-  int step = begin + wave;
+  int place = steps.begin + wave;
   Units units{};
   Pages pages{};
-  if (step < end) {
+  if (place < end) {
+    const int step = steps.step_at(place);
     units = table.units_of(step, table.pages_of(step));
-    pages = table.pages_of(step + 4);
+    pages = table.pages_of(steps.step_at(place + 4));
     load_keys(units);
     load_values(units);
   }
   r.start(a, raw);
 
-  for (; step < end; step += 4) {
+  for (; place < end; place += 4) {
     // The loads for the next step are always issued, after the last one for this step
     // again (out of the L2): behind a branch, every wait would have to assume the
     // fewest loads in flight, and wait for the newest.
-    const int next = step + 4 < end ? step + 4 : step;
+    const int step = steps.step_at(place), next = place + 4 < end ? place + 4 : place;
     const uint32_t found = units.found;
-    if (next > step) units = table.units_of(next, pages);
-    pages = table.pages_of(next + 4);
+    if (next > place) units = table.units_of(steps.step_at(next), pages);
+    pages = table.pages_of(steps.step_at(next + 4));
     each<4>([&](auto nn) {
       constexpr int n = decltype(nn)::value;
       half8_t k[C];
@@ -763,7 +817,7 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
     for (int g = 0; g < NG; ++g) vs[g] = sc.v[g];
     float cand[QT];
     if (masked) {
-      r.hide(step, found, work.w.keys, vs);
+      r.template hide<MORE>(step, found, work.w.keys, first, sinks, vs);
       r.template reach<true>(vs, cand);
     } else {
       r.template reach<false>(vs, cand);
@@ -823,7 +877,7 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum += ml[1][i][orow] * __builtin_amdgcn_exp2f(ml[0][i][orow] - mm);
-      const bool whole = work.chunks == 1;
+      const bool whole = work.chunks == 1 && !sched.partial;
       const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
       const int64_t at = (int64_t)(work.w.first + (uint32_t)flat / ratio) * heads * ratio + kh * ratio + (uint32_t)flat % ratio;
       float* const slot = ws.part + ((int64_t)work.slot * heads + kh) * partial_floats(TR, C);
@@ -857,9 +911,10 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
 // once a block: each wavefront turns its share of them into operands and leaves
 // those in LDS, in the lanes' order, for all, one step ahead of their use (two
 // buffers, one barrier a step).
-template <int C, int GC, int QT, bool AFF>
+template <int C, int GC, int QT, bool AFF, bool MORE>
 __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
   constexpr int NG = C / GC, DB = 16 * C, TR = kWideRows;
+  only_whole<MORE>(&a, &sched);
   constexpr int VJ = (C + 3) / 4;        // byte rows (of 16) of the values that a wavefront prepares
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
@@ -874,10 +929,11 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
   const bool rows_here = r.flat0 < r.flats;
   const Span all(a, work.w, work.tile * TR, TR);
   const Span span(a, work.w, rows_here ? r.flat0 : work.tile * TR, 16 * QT);
-  int begin, end;
-  chunk_steps(all.lo_first, all.hi_last, work.chunk, work.chunks, &begin, &end);
-  // the steps of which this wavefront's rows see something
+  const TileSteps<MORE> steps = tile_steps<MORE>(a, all.lo_first, all.hi_last, work.chunk, work.chunks).uniform();
+  const int end = steps.end, first_token = uniform(first_key(a)), sinks = uniform(sink_end(a));
+  // the steps of which this wavefront's rows see something, besides the first tokens
   const int first = span.lo_first / kStep, last = rows_here && span.hi_last > span.lo_first ? (span.hi_last - 1) / kStep : -1;
+  const int sink_steps = rows_here ? (sinks < span.hi_last ? sinks : span.hi_last) : 0;
   Words<4> raw[QT][C];
   r.load(a, work.w, kh, raw);
 
@@ -928,29 +984,30 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
     }
   };
 
-  int step = begin;
+  int place = steps.begin;
   Units units{};
   Pages pages{};
   uint32_t found = 0, found_next = 0;
-  if (step < end) {
-    units = table.units_of(step, table.pages_of(step));
-    pages = table.pages_of(step + 1);
+  if (place < end) {
+    units = table.units_of(steps.step_at(place), table.pages_of(steps.step_at(place)));
+    pages = table.pages_of(steps.step_at(place + 1));
     found = units.found;
     load(units);
   }
   r.start(a, raw);
-  if (step < end) {
+  if (place < end) {
     prepare(0);
     sc = sc_next;
-    if (step + 1 < end) units = table.units_of(step + 1, pages);
-    pages = table.pages_of(step + 2);
+    if (place + 1 < end) units = table.units_of(steps.step_at(place + 1), pages);
+    pages = table.pages_of(steps.step_at(place + 2));
     found_next = units.found;
     load(units);
     lds_barrier();
   }
 #pragma unroll 1
-  for (int buffer = 0; step < end; ++step, buffer ^= 1) {
-    if (step >= first && step <= last) {
+  for (int buffer = 0; place < end; ++place, buffer ^= 1) {
+    const int step = steps.step_at(place);
+    if ((step >= first && step <= last) || unit_token(step, 0) < (uint32_t)sink_steps) {
       // Operands are read from LDS one tile of keys, or one byte row of values, ahead
       // of the products that take them; the empty statements keep that order.
       half8_t k[2][C], v[2][4];
@@ -979,7 +1036,7 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
       for (int g = 0; g < NG; ++g) vs[g] = sc.v[g];
       float cand[QT];
       if (masked) {
-        r.hide(step, found, work.w.keys, vs);
+        r.template hide<MORE>(step, found, work.w.keys, first_token, sinks, vs);
         r.template reach<true>(vs, cand);
       } else {
         r.template reach<false>(vs, cand);
@@ -1004,8 +1061,8 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
     prepare(buffer ^ 1);                 // last read in the step before, which all have left
     sc = sc_next;
     found = found_next;
-    if (step + 2 < end) units = table.units_of(step + 2, pages);
-    pages = table.pages_of(step + 3);
+    if (place + 2 < end) units = table.units_of(steps.step_at(place + 2), pages);
+    pages = table.pages_of(steps.step_at(place + 3));
     found_next = units.found;
     load(units);
     lds_barrier();
@@ -1013,7 +1070,7 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
 
   if (!rows_here) return;
   const uint32_t ratio = (uint32_t)a.ratio;
-  const bool whole = work.chunks == 1;
+  const bool whole = work.chunks == 1 && !sched.partial;
   float* const slot = ws.part + ((int64_t)work.slot * heads + kh) * partial_floats(TR, C);
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
@@ -1047,9 +1104,12 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
   }
 }
 
+// Counts the blocks of each sequence of a large batch.
+hipError_t launch_cache_attention_plan(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream);
+
 // Defined for each width in a file of its own: launches the form for the cache's
-// groups and the schedule's tile height.
-template <int C>
+// groups and the schedule's tile height. MORE: see only_whole.
+template <int C, bool MORE>
 hipError_t launch_attention_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream);
 
 }  // namespace int4dq

@@ -1,0 +1,7 @@
+// cache_attention_more_256.hip -- the attention kernel for code rows of 256 channels, with
+// first tokens that stay visible and with parts of a batch that shares tokens.
+#include "cache_attention_launch.h"
+
+namespace int4dq {
+template hipError_t launch_attention_width<8, true>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
+}

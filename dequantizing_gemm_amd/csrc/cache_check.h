@@ -2,6 +2,7 @@
 // share (cache_api.cpp, cache_step_api.cpp). No HIP call is made here.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/int4dq_cache.h"
@@ -74,6 +75,40 @@ inline bool strides_ok(int64_t row_stride, int64_t head_stride) {
 // head and for each sequence and head, stays below 2^32 threads.
 inline bool call_fits(const RowsView& r, const CacheView& c, int64_t q_heads) {
   return r.rows * q_heads <= (int64_t(1) << 27) && (int64_t)r.batch * c.heads <= (int64_t(1) << 22);
+}
+
+// The arguments of attention, as kernels take them.
+inline int check_attention(const char* fn, const int4_cache_t* cache, const int4_cache_rows_t* rows, const void* q,
+                           int64_t q_row_stride, int64_t q_head_stride, int dtype, int64_t q_heads, float scale,
+                           int causal, int64_t window, void* out, float* lse, const void* workspace,
+                           int64_t workspace_bytes, AttentionArgs* a) {
+  CacheView c;
+  RowsView r;
+  const int rc = check_cache(fn, cache, rows, true, &c, &r);
+  if (rc != INT4DQ_OK) return rc;
+  if (dtype != INT4DQ_ROWS_F16 && dtype != INT4DQ_ROWS_BF16)
+    return fail(INT4DQ_EINVAL, "%s: dtype must be binary16 or bfloat16 (got %d)", fn, dtype);
+  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads)
+    return fail(INT4DQ_EINVAL, "%s: q_heads must be a multiple of heads, up to 65535 (got %lld, %d)", fn, (ll)q_heads, c.heads);
+  if (!call_fits(r, c, q_heads))
+    return fail(INT4DQ_EINVAL, "%s: rows * q_heads must be up to 2^27 and batch * heads up to 2^22", fn);
+  if (!isfinite(scale) || !(scale > 0.0f))
+    return fail(INT4DQ_EINVAL, "%s: scale must be finite and above 0 (got %g)", fn, (double)scale);
+  if (window < 0 || (window > 0 && !causal))
+    return fail(INT4DQ_EINVAL, "%s: window must be >= 0, and needs causal (got %lld)", fn, (ll)window);
+  if (!strides_ok(q_row_stride, q_head_stride))
+    return fail(INT4DQ_EINVAL, "%s: a stride is out of range", fn);
+  if (workspace_bytes < 0 || (workspace_bytes > 0 && !workspace))
+    return fail(INT4DQ_EINVAL, "%s: workspace_bytes must be >= 0, with a non-NULL workspace when > 0", fn);
+  if ((uintptr_t)workspace % 256) return fail(INT4DQ_EINVAL, "%s: workspace must be 256-byte aligned", fn);
+  if (r.rows > 0 && r.batch > 0 && (!q || !out)) return fail(INT4DQ_EINVAL, "%s: q and out must be non-NULL", fn);
+  const bool wide = (uintptr_t)q % 16 == 0 && c.D % 8 == 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0;
+  int scale_exp;
+  const float scale_part = (float)frexp((double)scale * 1.44269504088896340736, &scale_exp);
+  *a = AttentionArgs{c, r, q, q_row_stride, q_head_stride, dtype == INT4DQ_ROWS_BF16 ? 1 : 0, wide ? 1 : 0,
+                     (int)(q_heads / c.heads), scale_part, scale_exp, causal ? 1 : 0, window, out, lse,
+                     0, kWhole, nullptr, 0};
+  return INT4DQ_OK;
 }
 
 }  // namespace int4dq

@@ -31,6 +31,7 @@ struct Schedule {
   int units;                             // blocks per key/value head
   int crowded;                           // tiles may be more than the target by up to half
   int planned;                           // the blocks of each sequence are counted by a kernel of its own
+  int partial;                           // every block leaves a partial result, whole tiles too
 };
 
 // From more sequences than a wavefront looks through at once, their blocks are
@@ -60,11 +61,21 @@ struct SequenceWork {
   int steps;                             // of a tile, at most; 1 where there are none
 };
 
+// The first token of the part of the keys that a call sees, and the end of the first
+// tokens that stay visible with a window (0: none).
+__host__ __device__ inline int first_key(const AttentionArgs& a) {
+  return a.part == kOwnPart && *a.shared > 0 ? *a.shared : 0;
+}
+__host__ __device__ inline int sink_end(const AttentionArgs& a) {
+  return a.window <= 0 || a.sinks <= 0 ? 0 : a.sinks < INT32_MAX ? (int)a.sinks : INT32_MAX;
+}
+
 __host__ __device__ inline SequenceWork sequence_work(const AttentionArgs& a, int tile_rows, int b) {
   SequenceWork w;
-  const int s0 = a.r.starts ? a.r.starts[b] : b;
-  w.end = a.r.starts ? a.r.starts[b + 1] : b + 1;
-  w.length = a.r.lengths[b];
+  const bool all = a.part == kSharedPart;            // the rows of all sequences, the shared tokens' length
+  const int s0 = !a.r.starts ? b : a.r.starts[b];
+  w.end = a.r.starts ? a.r.starts[all ? a.all : b + 1] : all ? a.all : b + 1;
+  w.length = all ? *a.shared : a.r.lengths[b];
   w.first = s0 > 0 ? s0 : 0;
   const int last = w.end < a.r.rows ? w.end : (int)a.r.rows;
   w.rows = last > w.first ? last - w.first : 0;
@@ -72,12 +83,15 @@ __host__ __device__ inline SequenceWork sequence_work(const AttentionArgs& a, in
   w.keys = w.length < 0 ? 0 : w.length < cover ? w.length : (int)cover;
   w.tiles = (int)(((uint32_t)w.rows * (uint32_t)a.ratio + tile_rows - 1) / (uint32_t)tile_rows);
   w.steps = w.keys / kStep + (w.keys % kStep != 0);
-  if (a.window > 0 && a.window < w.keys) {
+  if (a.part == kOwnPart) w.steps -= first_key(a) / kStep;
+  if (a.part != kSharedPart && a.window > 0 && a.window < w.keys) {
     // a tile's rows lie on at most tile_rows / ratio + 2 positions
-    const int64_t run = (a.window + tile_rows / a.ratio + 2) / kStep + 2;
+    const int64_t sinks = (int64_t)sink_end(a) + kStep - 1;
+    const int64_t run = (a.window + tile_rows / a.ratio + 2) / kStep + 2 + sinks / kStep;
     if (run < w.steps) w.steps = (int)run;
   }
   if (w.steps < 1) w.steps = 1;
+  if (all && w.keys == 0) w.tiles = 0;               // nothing is shared
   return w;
 }
 
@@ -114,12 +128,33 @@ __host__ __device__ inline int steps_per_block(const Schedule& s, float work, fl
   return from;
 }
 
-// Keys [lo, hi) that row `token` of a sequence's rows sees.
+// Keys [lo, hi) that row `token` of a sequence's rows sees; with a window also those
+// of [first_key, sink_end) below hi, where lo does not reach down to them.
 __host__ __device__ inline void visible(const AttentionArgs& a, const SequenceWork& w, int token, int* lo,
                                         int* hi) {
-  const int64_t pos = (int64_t)w.length - w.end + w.first + token;
-  const int64_t top = a.causal && pos + 1 < w.keys ? pos + 1 : w.keys;
-  const int64_t low = a.window > 0 ? pos - a.window + 1 : 0;
+  int64_t pos = (int64_t)w.length - w.end + w.first + token;
+  int keys = w.keys;
+  if (a.part == kSharedPart) {                       // the row's own sequence
+    const int t = w.first + token;
+    int b = 0;
+    if (a.r.starts) {
+      int n = a.all;                                 // the last b with starts[b] <= t
+      while (n - b > 1) {
+        const int mid = (b + n) >> 1;
+        if (a.r.starts[mid] <= t) b = mid; else n = mid;
+      }
+    } else {
+      b = t < a.all ? t : a.all - 1;
+    }
+    const int length = a.r.lengths[b];
+    pos = (int64_t)length - (a.r.starts ? a.r.starts[b + 1] : b + 1) + t;
+    keys = length < 0 ? 0 : length < keys ? length : keys;
+  }
+  const int64_t top = a.causal && pos + 1 < keys ? pos + 1 : keys;
+  int64_t low = a.window > 0 ? pos - a.window + 1 : 0;
+  if (low <= sink_end(a)) low = 0;                   // no gap between the first tokens and the window
+  const int first = first_key(a);
+  if (low < first) low = first;
   *hi = top > 0 ? (int)top : 0;
   *lo = low < 0 ? 0 : low < *hi ? (int)low : *hi;
 }
@@ -131,6 +166,44 @@ __host__ __device__ inline void chunk_steps(int lo, int hi, int chunk, int chunk
   const int64_t from = s0 + (int64_t)chunk * per;
   *begin = from < s1 ? (int)from : s1;
   *end = from + per < s1 ? (int)(from + per) : s1;
+}
+
+// The same of a tile of which, with MORE, rows may also see the first tokens that stay
+// visible: their steps, `sinks` of them from the step `from` on, come before [lo, hi)'s,
+// and a block counts both in one run that begins so many places before lo's step:
+// places [begin, end), of which step_at gives the step.
+template <bool MORE>
+struct TileSteps {
+  int from, sinks, s0, begin, end;
+  __host__ __device__ __forceinline__ int step_at(int place) const {
+    return MORE && place < s0 ? place - (s0 - sinks) + from : place;
+  }
+  __device__ __forceinline__ TileSteps uniform() const {
+    auto u = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    return TileSteps{u(from), u(sinks), u(s0), u(begin), u(end)};
+  }
+};
+
+template <bool MORE>
+__host__ __device__ inline TileSteps<MORE> tile_steps(const AttentionArgs& a, int lo, int hi, int chunk, int chunks) {
+  TileSteps<MORE> t{0, 0, lo / kStep, 0, 0};
+  const int top = !MORE ? 0 : sink_end(a) < hi ? sink_end(a) : hi;
+  if (top == 0) {
+    chunk_steps(lo, hi, chunk, chunks, &t.begin, &t.end);
+    return t;
+  }
+  const int s1 = hi > lo ? (hi - 1) / kStep + 1 : t.s0;
+  t.from = first_key(a) / kStep;
+  int upto = (top - 1) / kStep + 1;
+  if (s1 > t.s0 && upto > t.s0) upto = t.s0;         // the others are among [lo, hi)'s
+  if (s1 == t.s0 && upto > t.s0) t.s0 = upto;        // there are none of [lo, hi)
+  t.sinks = upto > t.from && top > first_key(a) ? upto - t.from : 0;
+  const int run = t.sinks + (s1 > t.s0 ? s1 - t.s0 : 0), start = t.s0 - t.sinks;
+  const int per = chunks == 1 ? run : (int)((uint32_t)(run + chunks - 1) / (uint32_t)chunks);
+  const int64_t at = (int64_t)chunk * per;
+  t.begin = start + (at < run ? (int)at : run);
+  t.end = start + (at + per < run ? (int)(at + per) : run);
+  return t;
 }
 
 // Blocks of 32 channels to a scale in the kernel's form for this cache: all C, the
@@ -179,7 +252,9 @@ struct Workspace {
 
 __host__ __device__ inline int64_t partial_floats(int tile_rows, int C) { return (int64_t)tile_rows * (32 * C + 2); }
 
-__host__ __device__ inline int workspace_slots(const Schedule& s) { return (s.crowded ? 3 : 2) * s.target; }
+__host__ __device__ inline int workspace_slots(const Schedule& s) {
+  return s.partial ? s.units : (s.crowded ? 3 : 2) * s.target;
+}
 
 inline int64_t workspace_bytes(const Schedule& s, int heads, int C, int batch) {
   return workspace_slots(s) * (heads * partial_floats(s.tile_rows, C) * 4 + (int64_t)sizeof(PartRecord)) + 16 +

@@ -60,4 +60,13 @@ struct AppendArgs {
 
 hipError_t launch_cache_append(const AppendArgs& a, int dtype, hipStream_t stream);
 
+// ---------------------------------------------------------------- attention over shared tokens
+
+// Attention of a batch whose sequences begin with the same a.shared tokens; without
+// sharing where that would not pay, or the workspace is too small for it.
+hipError_t launch_cache_attention_shared(const AttentionArgs& a, void* workspace, int64_t workspace_bytes,
+                                         hipStream_t stream);
+// 0: a call of these sizes does not share.
+int64_t cache_attention_shared_workspace(const CacheView& c, const RowsView& r, int ratio);
+
 }  // namespace int4dq

@@ -13,9 +13,12 @@
 namespace {
 
 using int4dq::AppendArgs;
+using int4dq::AttentionArgs;
 using int4dq::CacheView;
 using int4dq::PagesArgs;
 using int4dq::RowsView;
+using int4dq::call_fits;
+using int4dq::check_attention;
 using int4dq::check_cache;
 using int4dq::fail;
 using int4dq::hip_status;
@@ -109,6 +112,41 @@ int int4_cache_append(const int4_cache_t* cache, const int4_cache_rows_t* rows, 
                      q_out, (int)q_heads, t.q_norm, t.k_norm, t.eps, t.rope, t.rope_stride, t.rope_positions,
                      t.rope ? (int)(t.rotary_dim / 2) : 0, t.interleaved ? 1 : 0};
   return hip_status(int4dq::launch_cache_append(a, dtype, (hipStream_t)stream), "int4_cache_append launch");
+}
+
+int int4_cache_attention_ex(const int4_cache_t* cache, const int4_cache_rows_t* rows, const void* q, int64_t q_row_stride,
+                            int64_t q_head_stride, int dtype, int64_t q_heads, float scale, int causal, int64_t window,
+                            int64_t sinks, const int32_t* shared, void* out, float* lse, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  const char* fn = "int4_cache_attention_ex";
+  AttentionArgs a;
+  const int rc = check_attention(fn, cache, rows, q, q_row_stride, q_head_stride, dtype, q_heads, scale, causal, window, out,
+                                 lse, workspace, workspace_bytes, &a);
+  if (rc != INT4DQ_OK) return rc;
+  if (sinks < 0) return fail(INT4DQ_EINVAL, "%s: sinks must be >= 0 (got %lld)", fn, (ll)sinks);
+  if (a.r.rows == 0 || a.r.batch == 0) return ok();
+  a.sinks = sinks;
+  a.shared = shared;
+  return hip_status(shared ? int4dq::launch_cache_attention_shared(a, workspace, workspace_bytes, (hipStream_t)stream)
+                           : int4dq::launch_cache_attention(a, workspace, workspace_bytes, (hipStream_t)stream),
+                    "int4_cache_attention_ex launch");
+}
+
+int64_t int4_cache_attention_ex_workspace_bytes(const int4_cache_t* cache, const int4_cache_rows_t* rows, int64_t q_heads,
+                                                int shares) {
+  const char* fn = "int4_cache_attention_ex_workspace_bytes";
+  CacheView c;
+  RowsView r;
+  if (check_cache(fn, cache, rows, false, &c, &r) != INT4DQ_OK) return -1;
+  if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads || !call_fits(r, c, q_heads)) {
+    fail(INT4DQ_EINVAL, "%s: q_heads must be a multiple of heads, rows * q_heads up to 2^27, batch * heads up to 2^22", fn);
+    return -1;
+  }
+  if (r.rows == 0 || r.batch == 0) return 0;
+  const int ratio = (int)(q_heads / c.heads);
+  const int64_t whole = int4dq::cache_attention_workspace(c, r, ratio);
+  const int64_t parts = shares ? int4dq::cache_attention_shared_workspace(c, r, ratio) : 0;
+  return whole > parts ? whole : parts;
 }
 
 }  // extern "C"

@@ -119,6 +119,36 @@ int int4_cache_append(const int4_cache_t *cache, const int4_cache_rows_t *rows,
                       int64_t k_head_stride, const void *v, int64_t v_row_stride, int64_t v_head_stride,
                       int dtype, void *q_out, void *stream);
 
+/*
+ * int4_cache_attention with first tokens that stay visible and first tokens that all
+ * sequences share.
+ *   sinks   with window > 0: a row at position p sees the keys j <= p with
+ *           j > p - window or j < sinks. Without a window it has no effect.
+ *   shared  in : [1], or NULL: every sequence begins with the same shared[0] tokens
+ *           (below 0: none). A sequence sees of them what it sees of its own (all
+ *           up to its length, its rows up to their positions). They are read through
+ *           the first row of page_table, whatever lengths[0] is, once for many
+ *           sequences where that pays: with few rows a sequence, and with a workspace
+ *           for it. The other entries of page_table that stand for them have to name
+ *           the same keys and values.
+ *   The arithmetic is that of int4_cache_attention; with shared tokens the two parts
+ *   of a row are joined in binary32.
+ * Errors: those of int4_cache_attention, and EINVAL for sinks < 0.
+ */
+int int4_cache_attention_ex(const int4_cache_t *cache, const int4_cache_rows_t *rows, const void *q,
+                            int64_t q_row_stride, int64_t q_head_stride, int dtype, int64_t q_heads,
+                            float scale, int causal, int64_t window, int64_t sinks,
+                            const int32_t *shared, void *out, float *lse, void *workspace,
+                            int64_t workspace_bytes, void *stream);
+
+/*
+ * As int4_cache_attention_workspace_bytes, of int4_cache_attention_ex; shares: 0 where
+ * `shared` will be NULL.
+ */
+int64_t int4_cache_attention_ex_workspace_bytes(const int4_cache_t *cache,
+                                                const int4_cache_rows_t *rows, int64_t q_heads,
+                                                int shares);
+
 #ifdef __cplusplus
 }
 #endif

@@ -103,3 +103,51 @@ def transform64(x, weight, eps, rope, interleaved):
         z[..., b] = size[..., b] * np.abs(c) + size[..., a] * np.abs(s)
         x, size = y, z
     return x, 5.0 * 2.0 ** -24 * size * (1 + 2.0 ** -20) + 2.0 ** -148
+
+
+class Sinks:
+    """Makes a cache model's attention (tests/cache_model.py) one with first tokens that
+    stay visible, from its own bounds: those tokens and the window's are all that a row's
+    part of the cache holds."""
+
+    def __init__(self, model, sinks):
+        self.model, self.sinks = model, sinks
+
+    def __getattr__(self, name):
+        return getattr(self.model, name)
+
+    def attend(self, q, table, lengths, starts, scale, causal=True, window=0):
+        m, rows = self.model, q.shape[0]
+        if not window:
+            return m.attend(q, table, lengths, starts, scale, causal, window)
+        out, tol = np.zeros(q.shape), np.zeros(q.shape)
+        lse, ltol = np.full(q.shape[:2], -np.inf), np.zeros(q.shape[:2])
+        owned = np.zeros(rows, bool)
+        for t in range(rows):
+            at = m.place(table, lengths, starts, t)
+            if at is None:
+                continue
+            owned[t] = True
+            b, pos, _ = at
+            top = min(pos + 1, int(lengths[b]))
+            # one row that sees all keys of a cache whose pages between the first tokens and
+            # the window are gone; tokens of the pages at the two borders one by one
+            gone = _Hidden(m, lambda j: self.sinks <= j <= pos - window)
+            o, l, _, tl, ll = gone.attend(q[t:t + 1], table[b:b + 1], [max(top, 0)], None, scale, False)
+            out[t], lse[t], tol[t], ltol[t] = o[0], l[0], tl[0], ll[0]
+        return out, lse, owned, tol, ltol
+
+
+class _Hidden:
+    """A model in which some positions have no page."""
+
+    def __init__(self, model, hides):
+        self.m, self.hides = model, hides
+        self.H, self.S = model.H, model.S
+        self.values, self.place = model.values, model.place
+
+    def page(self, table, b, pos):
+        return -1 if self.hides(pos) else self.m.page(table, b, pos)
+
+    def attend(self, *a):
+        return type(self.m).attend(self, *a)

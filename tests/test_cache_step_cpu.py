@@ -46,8 +46,8 @@ def test_pools_refused(change, needle):
 
 
 def test_page_calls_refused():
-    at = ctypes.addressof(cache_step._PoolStruct(**POOL))
-    L = dq.lib
+    pool = cache_step._PoolStruct(**POOL)
+    at, L = ctypes.addressof(pool), dq.lib
     for a in ((None, P, P, P, None, P, P), (at, None, P, P, None, P, P), (at, P, None, P, None, P, P),
               (at, P, P, None, None, P, P), (at, P, P, P, None, None, P), (at, P, P, P, None, P, None)):
         refused(L.int4_cache_release(*a, None), "non-NULL", "int4_cache_release")
