@@ -10,206 +10,168 @@
 // every product and sum rounded to binary32 by itself. The codes of a key go by the
 // last bit of this where a value lies next to a border between two codes; stated so,
 // and with a sum whose order does not show in binary32, they can be reproduced.
-#include "cache_rows.h"
-#include "cache_step.h"
-#include "lanes.h"
+#include "cache_append.h"
 #include "quantize_common.h"
 
 namespace int4dq {
 
 namespace {
 
-// What the kernels take besides the caller's arguments.
-struct AppendPlan {
-  RowArray q, k, v;
-  int out_wide;              // as RowArray::wide, of the output
-  int turn_wide;             // weights, cosines and sines of 8 channels lie 16-byte aligned, and their partners are 8 channels side by side
-  int group_lanes;           // lanes of a scale's group: 4, 8, 16 or 32
-  int64_t kv_blocks;         // steps: the first blocks; the others take queries
-  int q_heads_per_block, kv_heads_per_block;         // heads that a block takes in turn
-};
-
-// ---------------------------------------------------------------- norm and rotation
-
-template <int CTRL>
-__device__ __forceinline__ double add_dpp(double v) {
-  const u32x2_t x = __builtin_bit_cast(u32x2_t, v);
-  const uint32_t x0 = x.x, x1 = x.y;
-  u32x2_t y;
-  y.x = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x0, CTRL, 0xF, 0xF, true);
-  y.y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x1, CTRL, 0xF, 0xF, true);
-  return v + __builtin_bit_cast(double, y);
-}
-// Over LANES adjacent lanes (a power of two up to 32).
-template <int LANES>
-__device__ __forceinline__ double lanes_sum(double v) {
-  v = add_dpp<0xB1>(v);
-  v = add_dpp<0x4E>(v);
-  if constexpr (LANES >= 8) v = add_dpp<0x141>(v);
-  if constexpr (LANES >= 16) v = add_dpp<0x140>(v);
-  if constexpr (LANES >= 32) v += __shfl_xor(v, 16);
-  return v;
-}
-
-// binary32(1 / sqrt(m)): an estimate within 2^-20 and a step of third order, which
-// leaves 2^-52. At 0 and infinity the estimate, infinity and 0, is the value.
-__device__ __forceinline__ float norm_factor(double m) {
-  const double y = __builtin_amdgcn_rsq(m);
-  const double e = __builtin_fma(-m * y, y, 1.0);
-  const double better = __builtin_fma(y * e, __builtin_fma(e, 0.375, 0.5), y);
-  return (float)(m > 0.0 && m < __builtin_inf() ? better : y);
-}
-
-// The weights, cosines and sines of 8 channels from d on, and where their partners lie.
+// The weights, cosines and sines of 8 channels from d on, and where their partners
+// lie. WIDE, here and below: the rows' 8 channels lie 16-byte aligned in every array,
+// weights, cosines and sines as well, head_dim and half are multiples of 8, so that the
+// partners of 8 channels are 8 channels side by side.
+template <bool WIDE>
 struct Turn {
-  float w[8], wp[8], c[8], s[8];         // s: the sign of its product is in it
+  float w[8], c[8], s[8];                // s: the sign of its product is in it
+  float wp[WIDE ? 1 : 8];                // of the partners
   uint32_t turned;                       // a bit for each channel that is rotated
-  int partner;                           // of channel d, with halves; the others follow it
+  int partner;                           // WIDE, in halves: the lane of the wavefront that has the channels' partners
 
-  __device__ __forceinline__ void load(const AppendArgs& a, const AppendPlan& p, const float* norm, int64_t pos, int d) {
+  __device__ __forceinline__ void load(const AppendArgs& a, const float* norm, int64_t pos, int d) {
     const int D = a.c.D, half = a.rope ? a.half : 0;
     turned = 0;
-    partner = d;
-    if (p.turn_wide) {                   // head_dim and half are multiples of 8
+    partner = threadIdx.x & (kWave - 1);
+    if constexpr (WIDE) {
       const bool in = d < D, turn = d < 2 * half;
       const int at = in ? d : 0, pair = turn ? (a.interleaved ? d / 2 : d < half ? d : d - half) : 0;
       if (turn) turned = 0xFFu;
-      if (turn && !a.interleaved) partner = d < half ? d + half : d - half;
+      if (turn && !a.interleaved) partner += d < half ? half / 8 : -(half / 8);
       if (norm) {
-        const int other = in ? partner : 0;
-        const float4_t* const w4 = reinterpret_cast<const float4_t*>(norm + at);
-        const float4_t* const v4 = reinterpret_cast<const float4_t*>(norm + other);
+        const float4_t w0 = reinterpret_cast<const float4_t*>(norm + at)[0], w1 = reinterpret_cast<const float4_t*>(norm + at)[1];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[e] = w4[e / 4][e % 4];
-          wp[e] = a.interleaved ? w4[e / 4][(e ^ 1) % 4] : v4[e / 4][e % 4];
-        }
+        for (int e = 0; e < 8; ++e) w[e] = e < 4 ? w0[e % 4] : w1[e % 4];
       }
       if (half > 0) {
         const float* const row = a.rope + pos * a.rope_stride;
         const float4_t* const c4 = reinterpret_cast<const float4_t*>(row + pair);
         const float4_t* const s4 = reinterpret_cast<const float4_t*>(row + half + pair);
+        const float4_t c0 = c4[0], s0 = s4[0];
         if (a.interleaved) {
-          const float4_t x = c4[0], y = s4[0];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            c[e] = x[e / 2];
-            s[e] = e & 1 ? y[e / 2] : -y[e / 2];
+            c[e] = c0[e / 2];
+            s[e] = e & 1 ? s0[e / 2] : -s0[e / 2];
           }
         } else {
+          const float4_t c1 = c4[1], s1 = s4[1];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            c[e] = c4[e / 4][e % 4];
-            s[e] = d < half ? -s4[e / 4][e % 4] : s4[e / 4][e % 4];
+            const float x = e < 4 ? s0[e % 4] : s1[e % 4];
+            c[e] = e < 4 ? c0[e % 4] : c1[e % 4];
+            s[e] = d < half ? -x : x;
           }
         }
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int x = d + e;
-      const bool in = x < D, turn = x < 2 * half;
-      const int pair = !turn ? 0 : a.interleaved ? x / 2 : x < half ? x : x - half;
-      const int other = !turn ? x : a.interleaved ? x ^ 1 : x < half ? x + half : x - half;
-      if (turn) turned |= 1u << e;
-      if (norm) {
-        w[e] = norm[in ? x : 0];
-        wp[e] = norm[in ? other : 0];
-      }
-      if (half > 0) {
-        const float* const row = a.rope + pos * a.rope_stride;
-        c[e] = row[pair];
-        const float y = row[half + pair];
-        s[e] = (a.interleaved ? (x & 1) : x >= half) ? y : -y;
+      for (int e = 0; e < 8; ++e) {
+        const int x = d + e;
+        const bool in = x < D, turn = x < 2 * half;
+        const int pair = !turn ? 0 : a.interleaved ? x / 2 : x < half ? x : x - half;
+        const int other = !turn ? x : a.interleaved ? x ^ 1 : x < half ? x + half : x - half;
+        if (turn) turned |= 1u << e;
+        if (norm) {
+          w[e] = norm[in ? x : 0];
+          wp[e] = norm[in ? other : 0];
+        }
+        if (half > 0) {
+          const float* const row = a.rope + pos * a.rope_stride;
+          c[e] = row[pair];
+          const float y = row[half + pair];
+          s[e] = (a.interleaved ? (x & 1) : x >= half) ? y : -y;
+        }
       }
     }
   }
 };
 
-// The partners of 8 channels from d on in the halves' form (of a channel that has
-// none, itself), from the row in memory: it was read just before.
-template <int DT>
-__device__ __forceinline__ void load_partners(const AppendArgs& a, const AppendPlan& p, const Turn& t, const Bits<DT>* src,
-                                              int wide, int d, Bits<DT> raw[8]) {
-  if (wide && p.turn_wide) {
-    const auto v = *reinterpret_cast<const Pack<Bits<DT>, 8>*>(src + (t.partner < a.c.D ? t.partner : 0));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) raw[e] = v.v[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int x = d + e, other = x >= 2 * a.half ? x : x < a.half ? x + a.half : x - a.half;
-      raw[e] = src[other < a.c.D ? other : 0];
-    }
-  }
+// From the lane that has the partners of a lane's channels.
+template <int L>
+__device__ __forceinline__ float of_partner(const AppendArgs& a, int partner, float v) {
+  if (L == 16 && a.half == 64)                       // the same for all: 128 channels in halves of a row's 16 lanes
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
+  return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(4 * partner, __builtin_bit_cast(int, v)));
 }
 
-// Normalised and rotated values of 8 channels from d on; 0 from head_dim on.
-__device__ __forceinline__ void turn8(const AppendArgs& a, const Turn& t, bool normed, float r, int d, const float x[8],
-                                      const float xp[8], float y[8]) {
+// A lane's 8 channels of a row as they lie in memory (from head_dim on, some other
+// channel), and where not WIDE their partners in the halves' form (of a channel that
+// has none, itself).
+template <int DT, bool WIDE>
+struct Raw {
+  Bits<DT> v[8], p[WIDE ? 1 : 8];
+
+  __device__ __forceinline__ void load(const Bits<DT>* src, int d, int D) {
+    if constexpr (WIDE) {
+      const auto x = *reinterpret_cast<const Pack<Bits<DT>, 8>*>(src + (d < D ? d : 0));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = x.v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = src[d + e < D ? d + e : 0];
+    }
+  }
+  __device__ __forceinline__ void load_partners(const AppendArgs& a, const Bits<DT>* src, int d) {
+    if constexpr (!WIDE) {
+      if (a.interleaved || !a.rope) return;          // the same for all
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int x = d + e, other = x >= 2 * a.half ? x : x < a.half ? x + a.half : x - a.half;
+        p[e] = src[other < a.c.D ? other : 0];
+      }
+    }
+  }
+  // 0 from head_dim on
+  __device__ __forceinline__ void values(int d, int D, float x[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (WIDE ? d : d + e) < D ? value_of<DT>(v[e]) : 0.0f;
+  }
+};
+
+// A row's head of queries or keys: normalises and rotates a lane's 8 channels; 0 from
+// head_dim on. All L lanes take part.
+template <int DT, int L, bool WIDE>
+__device__ __forceinline__ void transformed(const AppendArgs& a, const AppendPlan& p, const Turn<WIDE>& t, bool normed,
+                                            const Raw<DT, WIDE>& raw, int d, float y[8]) {
 #pragma clang fp contract(off)
-  float n[8], np[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    n[e] = normed ? (x[e] * r) * t.w[e] : x[e];
-    np[e] = normed ? (xp[e] * r) * t.wp[e] : xp[e];
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float own = n[e] * t.c[e], other = np[e] * t.s[e];
-    const float z = (t.turned >> e) & 1u ? own + other : n[e];
-    y[e] = d + e < a.c.D ? z : 0.0f;
-  }
-}
-
-// The partners' values of a lane's 8 channels.
-template <int DT>
-__device__ __forceinline__ void partners_of(const AppendArgs& a, const AppendPlan& p, const Turn& t, const Bits<DT>* src,
-                                            int wide, int d, const float x[8], float xp[8]) {
-  if (a.interleaved || !a.rope) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
-  } else {
-    Bits<DT> raw[8];
-    load_partners<DT>(a, p, t, src, wide, d, raw);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) xp[e] = value_of<DT>(raw[e]);
-  }
-}
-
-// A lane's 8 channels of a row; 0 from head_dim on.
-template <int DT>
-__device__ __forceinline__ void load_channels(const Bits<DT>* src, int wide, int d, int D, float x[8]) {
-  if (wide) {
-    const bool in = d < D;
-    const auto v = *reinterpret_cast<const Pack<Bits<DT>, 8>*>(src + (in ? d : 0));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = in ? value_of<DT>(v.v[e]) : 0.0f;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const Bits<DT> v = src[d + e < D ? d + e : 0];
-      x[e] = d + e < D ? value_of<DT>(v) : 0.0f;
-    }
-  }
-}
-
-// A row's head of queries or keys: loads, normalises and rotates a lane's 8 channels.
-template <int DT, int L>
-__device__ __forceinline__ void transformed(const AppendArgs& a, const AppendPlan& p, const Turn& t, bool normed,
-                                            const Bits<DT>* src, int wide, int d, float y[8]) {
-  float x[8], xp[8];
-  load_channels<DT>(src, wide, d, a.c.D, x);
-  partners_of<DT>(a, p, t, src, wide, d, x, xp);
   float r = 1.0f;
+  raw.values(d, a.c.D, y);
   if (normed) {
     double sum = 0.0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)x[e], (double)x[e], sum);
-    r = norm_factor(lanes_sum<L>(sum) / (double)a.c.D + a.eps);
+    for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)y[e], (double)y[e], sum);
+    r = norm_factor(lanes_sum<L>(sum) * p.mean + a.eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (y[e] * r) * t.w[e];
   }
-  turn8(a, t, normed, r, d, x, xp, y);
+  if (a.rope) {
+    float other[8];
+    if (a.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = y[e ^ 1];
+    } else if constexpr (WIDE) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = of_partner<L>(a, t.partner, y[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        other[e] = value_of<DT>(raw.p[e]);
+        if (normed) other[e] = (other[e] * r) * t.wp[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = y[e] * t.c[e], z = other[e] * t.s[e], turned = x + z;
+      y[e] = (WIDE ? t.turned != 0 : (t.turned >> e) & 1u) ? turned : y[e];
+    }
+  }
+  if constexpr (!WIDE) {                             // weights of other channels have been there
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = d + e < a.c.D ? y[e] : 0.0f;
+  } else if (a.c.D < 8 * L) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = d < a.c.D ? y[e] : 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------- codes
@@ -249,29 +211,35 @@ __device__ __forceinline__ Codes codes_of(const AppendArgs& a, const AppendPlan&
   const _Float16 s16 = (_Float16)(AFF ? (hi - lo) / 15.0f : hi / 7.0f);
   const float sf = (float)s16, rsf = scale_rcp(sf);
   const uint32_t zp = AFF ? affine_zp(lo, sf) : 0u;
-  float code[8];
-  bool near = false;
+  // codes of quantize_common.h's code_of and affine_code, from 0 up (symmetric ones plus
+  // 8), with one branch around the divisions: |t - rint(t)| is at most a half, and
+  // where it is that within 2^-14 the quotient decides
+  constexpr float kZero = AFF ? 0.0f : 8.0f;
+  const float up = AFF ? (float)zp : kZero;
+  float code[8], most = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float t = x[e] * rsf, n = __builtin_rintf(t);
-    near |= __builtin_fabsf(__builtin_fabsf(t - n) - 0.5f) < 0x1p-14f;           // near_half_integer(t)
-    code[e] = AFF ? __builtin_fminf(__builtin_fmaxf(n + (float)zp, 0.0f), 15.0f)
-                  : __builtin_fminf(__builtin_fmaxf(n, -8.0f), 7.0f);
+    most = __builtin_fmaxf(most, __builtin_fabsf(t - n));
+    code[e] = __builtin_amdgcn_fmed3f(n + up, 0.0f, 15.0f);
   }
-  if (__builtin_expect(near, 0)) {
+  if (__builtin_expect(most > 0.5f - 0x1p-14f, 0)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (near_half_integer(x[e] * rsf))
         code[e] = AFF ? (float)affine_code(x[e], sf, rsf, zp)
-                      : __builtin_fminf(__builtin_fmaxf(__builtin_rintf(x[e] / sf), -8.0f), 7.0f);   // IEEE division
+                      : __builtin_fminf(__builtin_fmaxf(__builtin_rintf(x[e] / sf), -8.0f), 7.0f) + kZero;   // IEEE division
   }
-  Codes q{0, __builtin_bit_cast(uint16_t, s16), (uint8_t)zp};
+  if (AFF && a.c.D % 8 != 0)                         // padding channels have code 0
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t u = (uint32_t)(int)code[e] & 15u;
-    q.word |= (!AFF || d + e < a.c.D ? u : 0u) << (4 * e);                         // padding channels have code 0
-  }
-  return q;
+    for (int e = 0; e < 8; ++e) code[e] = d + e < a.c.D ? code[e] : 0.0f;
+  // four nibbles are a whole number below 2^16, exact in binary32
+  auto four = [&](int e) {
+    return (uint32_t)__builtin_fmaf(__builtin_fmaf(__builtin_fmaf(code[e + 3], 16.0f, code[e + 2]), 16.0f, code[e + 1]), 16.0f, code[e]);
+  };
+  const uint32_t word = four(0) | four(4) << 16;
+  // two's complement: the highest bit of a nibble the other way round; code 0 is 8 from 0 up
+  return Codes{AFF ? (d < a.c.D ? word : 0u) : word ^ 0x88888888u, __builtin_bit_cast(uint16_t, s16), (uint8_t)zp};
 }
 __device__ __forceinline__ Codes codes_of(const AppendArgs& a, const AppendPlan& p, int d, const float x[8]) {
   return a.c.affine ? codes_of<true>(a, p, d, x) : codes_of<false>(a, p, d, x);
@@ -294,35 +262,42 @@ __device__ __forceinline__ void store_key(const CacheView& c, const Codes& q, in
 
 // ---------------------------------------------------------------- rows
 
-__device__ __forceinline__ bool position_there(const AppendArgs& a, int64_t pos) {
-  return pos >= 0 && (!a.rope || pos < a.positions);
-}
-
-// A lane's 8 channels of the output.
+// Two outputs as binary16 or bfloat16 patterns, rounded to nearest even.
 template <int DT>
-__device__ __forceinline__ void store_query(const AppendArgs& a, const AppendPlan& p, int64_t row, int head, int d,
-                                            const float y[8]) {
-  Bits<DT>* const to = static_cast<Bits<DT>*>(a.out) + (row * a.q_heads + head) * a.c.D + d;
-  Pack<Bits<DT>, 8> out;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) out.v[e] = bits_of<DT>(y[e]);
-  if (p.out_wide) {
-    if (d < a.c.D) *reinterpret_cast<Pack<Bits<DT>, 8>*>(to) = out;
+__device__ __forceinline__ uint32_t pair_of(float x, float y) {
+  if constexpr (DT == INT4DQ_ROWS_BF16) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const bf16x2_t v = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, v);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (d + e < a.c.D) to[e] = out.v[e];
+    const half2_t v = {(_Float16)x, (_Float16)y};
+    return __builtin_bit_cast(uint32_t, v);
   }
 }
 
-template <int DT>
-__device__ __forceinline__ const Bits<DT>* at_row(const RowArray& x, int64_t row, int head) {
-  return static_cast<const Bits<DT>*>(x.p) + row * x.row_stride + head * x.head_stride;
+// A lane's 8 channels of the output.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void store_query(const AppendArgs& a, int64_t row, int head, int d, const float y[8]) {
+  Bits<DT>* const to = static_cast<Bits<DT>*>(a.out) + (row * a.q_heads + head) * a.c.D + d;
+  if constexpr (WIDE) {
+    if (d >= a.c.D) return;
+    if constexpr (DT == INT4DQ_ROWS_F32) {
+      reinterpret_cast<float4_t*>(to)[0] = float4_t{y[0], y[1], y[2], y[3]};
+      reinterpret_cast<float4_t*>(to)[1] = float4_t{y[4], y[5], y[6], y[7]};
+    } else {
+      *reinterpret_cast<u32x4_t*>(to) = u32x4_t{pair_of<DT>(y[0], y[1]), pair_of<DT>(y[2], y[3]), pair_of<DT>(y[4], y[5]),
+                                                pair_of<DT>(y[6], y[7])};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (d + e < a.c.D) to[e] = bits_of<DT>(y[e]);
+  }
 }
 
 // Where sequences have few rows: L lanes for one head of a row's queries, keys or
 // values, in this order. Value codes leave byte by byte.
-template <int DT, int L>
+template <int DT, int L, bool WIDE>
 __global__ __launch_bounds__(256) void cache_append_rows_kernel(AppendArgs a, AppendPlan p) {
   const CacheView& c = a.c;
   const int lane = threadIdx.x & (L - 1), d = 8 * lane, all = a.q_heads + 2 * c.heads;
@@ -331,29 +306,29 @@ __global__ __launch_bounds__(256) void cache_append_rows_kernel(AppendArgs a, Ap
   int seq = 0;
   int64_t pos = -1;
   if (row >= a.r.rows || !find_row(a.r, row, &seq, &pos)) return;                  // the same for the L lanes
-  const bool there = position_there(a, pos);
-  if (which < a.q_heads) {
-    float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (there) {
-      Turn t;
-      t.load(a, p, a.q_norm, pos, d);
-      transformed<DT, L>(a, p, t, a.q_norm != nullptr, at_row<DT>(p.q, row, which), p.q.wide, d, y);
+  const bool there = position_there(a, pos), query = which < a.q_heads, keys = !query && which < a.q_heads + c.heads;
+  const int head = query ? which : which - a.q_heads - (keys ? 0 : c.heads);
+  const RowArray& in = query ? p.q : keys ? p.k : p.v;
+  const float* const norm = query ? a.q_norm : a.k_norm;
+  const Bits<DT>* const src = at_row<DT>(in, row, head);
+  float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (there) {
+    Raw<DT, WIDE> raw;
+    raw.load(src, d, c.D);
+    if (query || keys) {
+      Turn<WIDE> t;
+      t.load(a, norm, pos, d);
+      raw.load_partners(a, src, d);
+      transformed<DT, L, WIDE>(a, p, t, norm != nullptr, raw, d, y);
+    } else {
+      raw.values(d, c.D, y);
     }
-    return store_query<DT>(a, p, row, which, d, y);
   }
+  if (query) return store_query<DT, WIDE>(a, row, head, d, y);
   const int64_t page = there ? find_page(a.r, c, seq, pos) : -1;
   if (page < 0) return;
-  const bool keys = which < a.q_heads + c.heads;
-  const int head = which - a.q_heads - (keys ? 0 : c.heads), ts = (int)(pos & 15);
+  const int ts = (int)(pos & 15);
   const int64_t unit = c.unit(page, head, (int)(pos & (((int64_t)1 << c.page_shift) - 1)));
-  float y[8];
-  if (keys) {
-    Turn t;
-    t.load(a, p, a.k_norm, pos, d);
-    transformed<DT, L>(a, p, t, a.k_norm != nullptr, at_row<DT>(p.k, row, head), p.k.wide, d, y);
-  } else {
-    load_channels<DT>(at_row<DT>(p.v, row, head), p.v.wide, d, c.D, y);
-  }
   const Codes q = codes_of(a, p, d, y);
   store_scale(a, p, q, keys, unit, ts, lane);
   if (keys) {
@@ -367,153 +342,114 @@ __global__ __launch_bounds__(256) void cache_append_rows_kernel(AppendArgs a, Ap
 
 // ---------------------------------------------------------------- prompts
 
-// 64 positions of a sequence (find_store_block), several heads of one side in turn.
-// Value codes go through LDS and leave as 16-byte rows of a unit; a unit of which
-// some tokens are not written leaves byte by byte.
-template <int DT, int L>
-__device__ __forceinline__ void append_step(const AppendArgs& a, const AppendPlan& p, int64_t block, uint8_t (*bytes)[4 * 128 * 16],
-                                            int64_t units[4], uint32_t* written) {
-  constexpr int ROWS = 256 / L;
+// Keys whose pairs lie in two threads of cache_append_keys.hip: 64 positions of a
+// sequence (find_store_block), one head, L lanes a row.
+template <int DT, int L, bool WIDE>
+__device__ __forceinline__ void append_keys(const AppendArgs& a, const AppendPlan& p, int64_t block) {
   const CacheView& c = a.c;
-  const int chunks = (c.heads + p.kv_heads_per_block - 1) / p.kv_heads_per_block;
-  const bool keys = block & 1;
-  const int head0 = (int)((block >> 1) % chunks) * p.kv_heads_per_block;
-  const int head1 = head0 + p.kv_heads_per_block < c.heads ? head0 + p.kv_heads_per_block : c.heads;
+  const int head = (int)(block % c.heads);
   StoreBlock w;
-  if (!find_store_block(a.r, (int)((block >> 1) / chunks), LaneSearch{}, &w)) return;
-  const int tid = threadIdx.x, lane = tid & (L - 1), d = 8 * lane, DB = 16 * c.C;
-  const int page_units = 1 << (c.page_shift - 4);
-  if (tid < 4) {
-    const int64_t pos = w.base + 16 * tid, page = find_page(a.r, c, w.b, pos);
-    units[tid] = page < 0 ? -1 : c.unit(page, 0, (int)(pos & (((int64_t)1 << c.page_shift) - 1)));
-  }
-  __syncthreads();
-  auto token_there = [&](int token) {
+  if (!find_store_block(a.r, (int)(block / c.heads), LaneSearch{}, &w)) return;
+  const int lane = threadIdx.x & (L - 1), d = 8 * lane;
+#pragma unroll 1
+  for (int token = threadIdx.x / L; token < 64; token += 256 / L) {
     const int64_t pos = w.base + token, at = pos - w.p0;
-    return at >= 0 && at < w.rows && units[token >> 4] >= 0 && position_there(a, pos);
-  };
-  if (keys) {
-#pragma unroll 1
-    for (int token = tid / L; token < 64; token += ROWS) {
-      if (!token_there(token)) continue;
-      const int64_t pos = w.base + token, row = w.first + (pos - w.p0);
-      Turn t;
-      t.load(a, p, a.k_norm, pos, d);
-#pragma unroll 1
-      for (int head = head0; head < head1; ++head) {
-        float y[8];
-        transformed<DT, L>(a, p, t, a.k_norm != nullptr, at_row<DT>(p.k, row, head), p.k.wide, d, y);
-        const Codes q = codes_of(a, p, d, y);
-        const int64_t unit = units[token >> 4] + (int64_t)head * page_units;
-        store_scale(a, p, q, true, unit, token & 15, lane);
-        store_key(c, q, unit, token & 15, lane);
-      }
-    }
-    return;
-  }
-  if (tid < kWave) {
-    const uint64_t there = __ballot(token_there(tid));
-    if (tid < 4) written[tid] = (uint32_t)(there >> (16 * tid)) & 0xFFFFu;
-  }
-#pragma unroll 1
-  for (int head = head0, turn = 0; head < head1; ++head, turn ^= 1) {
-#pragma unroll 1
-    for (int token = tid / L; token < 64; token += ROWS) {
-      if (!token_there(token)) continue;
-      const int64_t row = w.first + (w.base + token - w.p0);
-      float y[8];
-      load_channels<DT>(at_row<DT>(p.v, row, head), p.v.wide, d, c.D, y);
-      const Codes q = codes_of(a, p, d, y);
-      store_scale(a, p, q, false, units[token >> 4] + (int64_t)head * page_units, token & 15, lane);
-      if (lane < 4 * c.C)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          bytes[turn][((token >> 4) * DB + 4 * lane + k) * 16 + (token & 15)] = (uint8_t)(q.word >> (8 * k));
-    }
-    __syncthreads();                     // two buffers: the one written next was read before this
-    for (int it = tid; it < 4 * DB; it += 256) {
-      const int u = it / DB, j = it % DB;
-      uint32_t mask = written[u];
-      if (mask == 0) continue;
-      uint8_t* const to = c.v_packed + (units[u] + (int64_t)head * page_units) * (16 * DB) + j * 16;
-      if (mask == 0xFFFFu) {
-        *reinterpret_cast<u32x4_t*>(to) = *reinterpret_cast<const u32x4_t*>(&bytes[turn][it * 16]);
-      } else {
-        for (; mask; mask &= mask - 1) {
-          const int t = __builtin_ctz(mask);
-          to[t] = bytes[turn][it * 16 + t];
-        }
-      }
-    }
+    if (at < 0 || at >= w.rows || !position_there(a, pos)) continue;               // the same for the L lanes
+    const int64_t page = find_page(a.r, c, w.b, pos);
+    if (page < 0) continue;
+    const int64_t unit = c.unit(page, head, (int)(pos & (((int64_t)1 << c.page_shift) - 1)));
+    const Bits<DT>* const src = at_row<DT>(p.k, w.first + at, head);
+    Raw<DT, WIDE> raw;
+    raw.load(src, d, c.D);
+    raw.load_partners(a, src, d);
+    Turn<WIDE> t;
+    t.load(a, a.k_norm, pos, d);
+    float y[8];
+    transformed<DT, L, WIDE>(a, p, t, a.k_norm != nullptr, raw, d, y);
+    const Codes q = codes_of(a, p, d, y);
+    store_scale(a, p, q, true, unit, token & 15, lane);
+    store_key(c, q, unit, token & 15, lane);
   }
 }
 
 // Rows of queries, L lanes a row, several heads in turn.
-template <int DT, int L>
+template <int DT, int L, bool WIDE>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, const AppendPlan& p, int64_t block) {
-  const int chunks = (a.q_heads + p.q_heads_per_block - 1) / p.q_heads_per_block;
+  const int chunks = (a.q_heads + p.heads_per_block - 1) / p.heads_per_block;
   const int64_t row = block / chunks * (256 / L) + threadIdx.x / L;
-  const int head0 = (int)(block % chunks) * p.q_heads_per_block;
-  const int head1 = head0 + p.q_heads_per_block < a.q_heads ? head0 + p.q_heads_per_block : a.q_heads;
+  const int head0 = (int)(block % chunks) * p.heads_per_block;
+  const int head1 = head0 + p.heads_per_block < a.q_heads ? head0 + p.heads_per_block : a.q_heads;
   const int d = (threadIdx.x & (L - 1)) * 8;
   int seq = 0;
   int64_t pos = -1;
   if (row >= a.r.rows || !find_row(a.r, row, &seq, &pos)) return;                  // the same for the L lanes
   const bool there = position_there(a, pos);
-  Turn t;
-  t.load(a, p, a.q_norm, there ? pos : 0, d);
+  Turn<WIDE> t;
+  t.load(a, a.q_norm, there ? pos : 0, d);
+  const Bits<DT>* src = at_row<DT>(p.q, row, head0);
+  Raw<DT, WIDE> next;
+  next.load(src, d, a.c.D);
+  next.load_partners(a, src, d);
 #pragma unroll 1
   for (int head = head0; head < head1; ++head) {
+    const Raw<DT, WIDE> raw = next;
+    src += head + 1 < head1 ? p.q.head_stride : 0;               // (the last one's again, for no one)
+    next.load(src, d, a.c.D);
+    next.load_partners(a, src, d);
     float y[8];
-    transformed<DT, L>(a, p, t, a.q_norm != nullptr, at_row<DT>(p.q, row, head), p.q.wide, d, y);
+    transformed<DT, L, WIDE>(a, p, t, a.q_norm != nullptr, raw, d, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = there ? y[e] : 0.0f;
-    store_query<DT>(a, p, row, head, d, y);
+    store_query<DT, WIDE>(a, row, head, d, y);
   }
 }
 
-template <int DT, int L>
+template <int DT, int L, bool WIDE>
 __global__ __launch_bounds__(256) void cache_append_steps_kernel(AppendArgs a, AppendPlan p) {
-  __shared__ __attribute__((aligned(16))) uint8_t bytes[2][4 * 128 * 16];            // [unit][channel pair][token]
-  __shared__ int64_t units[4];
-  __shared__ uint32_t written[4];                    // a bit for each token of the unit
   const int64_t block = blockIdx.x;
-  if (block < p.kv_blocks) append_step<DT, L>(a, p, block, bytes, units, written);
-  else append_queries<DT, L>(a, p, block - p.kv_blocks);
+  if (block < p.key_blocks) append_keys<DT, L, WIDE>(a, p, block);
+  else append_queries<DT, L, WIDE>(a, p, block - p.key_blocks);
 }
 
 // ---------------------------------------------------------------- launches
 
-template <int DT, int L>
-void launch_lanes(const AppendArgs& a, AppendPlan p, hipStream_t stream) {
+template <int DT, int L, bool WIDE>
+hipError_t launch_lanes(const AppendArgs& a, AppendPlan p, int dtype, hipStream_t stream) {
   constexpr int ROWS = 256 / L;
   if (!a.r.starts || a.r.rows < 8 * (int64_t)a.r.batch) {
     const int64_t items = a.r.rows * (a.q_heads + 2 * a.c.heads);
-    hipLaunchKernelGGL((cache_append_rows_kernel<DT, L>), dim3((unsigned)((items + ROWS - 1) / ROWS)), dim3(256), 0, stream,
-                       a, p);
-    return;
+    hipLaunchKernelGGL((cache_append_rows_kernel<DT, L, WIDE>), dim3((unsigned)((items + ROWS - 1) / ROWS)), dim3(256), 0,
+                       stream, a, p);
+    return hipGetLastError();
   }
+  const bool keys = keys_in_thread(a) && WIDE;
+  const hipError_t e = launch_cache_append_quads(a, p, dtype, keys, stream);
+  if (e != hipSuccess) return e;
   // Several heads a block, which share cosines and sines, as long as that leaves twice
   // the 2048 blocks that the GPU holds at once.
-  auto per_block = [](int64_t blocks, int heads) {
-    int n = 1;
-    while (n < 8 && blocks * (heads / (2 * n)) >= 4096) n *= 2;
-    return n;
-  };
-  const int64_t units = store_units(a.r), row_blocks = (a.r.rows + ROWS - 1) / ROWS;
-  p.kv_heads_per_block = per_block(2 * units, a.c.heads);
-  p.q_heads_per_block = per_block(row_blocks, a.q_heads);
-  p.kv_blocks = 2 * units * ((a.c.heads + p.kv_heads_per_block - 1) / p.kv_heads_per_block);
-  const int64_t blocks = p.kv_blocks + row_blocks * ((a.q_heads + p.q_heads_per_block - 1) / p.q_heads_per_block);
-  hipLaunchKernelGGL((cache_append_steps_kernel<DT, L>), dim3((unsigned)blocks), dim3(256), 0, stream, a, p);
+  const int64_t row_blocks = (a.r.rows + ROWS - 1) / ROWS;
+  p.heads_per_block = 1;
+  while (p.heads_per_block < 8 && row_blocks * (a.q_heads / (2 * p.heads_per_block)) >= 4096) p.heads_per_block *= 2;
+  p.key_blocks = keys ? 0 : store_units(a.r) * a.c.heads;
+  const int64_t blocks = p.key_blocks + row_blocks * ((a.q_heads + p.heads_per_block - 1) / p.heads_per_block);
+  hipLaunchKernelGGL((cache_append_steps_kernel<DT, L, WIDE>), dim3((unsigned)blocks), dim3(256), 0, stream, a, p);
+  return hipGetLastError();
+}
+
+template <int DT, bool WIDE>
+hipError_t launch_width(const AppendArgs& a, const AppendPlan& p, int dtype, hipStream_t stream) {
+  if (a.c.C <= 2) return launch_lanes<DT, 8, WIDE>(a, p, dtype, stream);
+  if (a.c.C <= 4) return launch_lanes<DT, 16, WIDE>(a, p, dtype, stream);
+  return launch_lanes<DT, 32, WIDE>(a, p, dtype, stream);
 }
 
 template <int DT>
-hipError_t launch_type(const AppendArgs& a, const AppendPlan& p, hipStream_t stream) {
-  if (a.c.C <= 2) launch_lanes<DT, 8>(a, p, stream);
-  else if (a.c.C <= 4) launch_lanes<DT, 16>(a, p, stream);
-  else launch_lanes<DT, 32>(a, p, stream);
-  return hipGetLastError();
+hipError_t launch_type(const AppendArgs& a, const AppendPlan& p, int dtype, hipStream_t stream) {
+  const bool turn_wide = ((uintptr_t)a.q_norm | (uintptr_t)a.k_norm | (uintptr_t)a.rope) % 16 == 0 &&
+                         (!a.rope || (a.half % 8 == 0 && a.rope_stride % 4 == 0));
+  if (p.q.wide && p.k.wide && p.v.wide && turn_wide && (uintptr_t)a.out % 16 == 0)
+    return launch_width<DT, true>(a, p, dtype, stream);
+  return launch_width<DT, false>(a, p, dtype, stream);
 }
 
 }  // namespace
@@ -524,14 +460,12 @@ hipError_t launch_cache_append(const AppendArgs& a, int dtype, hipStream_t strea
     const int wide = a.c.D % 8 == 0 && (uintptr_t)x % 16 == 0 && row_stride % per16 == 0 && head_stride % per16 == 0;
     return RowArray{const_cast<void*>(x), row_stride, head_stride, wide};
   };
-  AppendPlan p{rows(a.q, a.q_row_stride, a.q_head_stride), rows(a.k, a.k_row_stride, a.k_head_stride),
-               rows(a.v, a.v_row_stride, a.v_head_stride), a.c.D % 8 == 0 && (uintptr_t)a.out % 16 == 0, 0, 0, 0, 1, 1};
-  p.turn_wide = a.c.D % 8 == 0 && ((uintptr_t)a.q_norm | (uintptr_t)a.k_norm | (uintptr_t)a.rope) % 16 == 0 &&
-                (!a.rope || (a.half % 8 == 0 && a.rope_stride % 4 == 0));
-  p.group_lanes = a.c.G > 1 ? a.c.group / 8 : a.c.C <= 2 ? 8 : a.c.C <= 4 ? 16 : 32;
-  if (dtype == INT4DQ_ROWS_F32) return launch_type<INT4DQ_ROWS_F32>(a, p, stream);
-  if (dtype == INT4DQ_ROWS_F16) return launch_type<INT4DQ_ROWS_F16>(a, p, stream);
-  return launch_type<INT4DQ_ROWS_BF16>(a, p, stream);
+  const int lanes = a.c.G > 1 ? a.c.group / 8 : a.c.C <= 2 ? 8 : a.c.C <= 4 ? 16 : 32;
+  const AppendPlan p{rows(a.q, a.q_row_stride, a.q_head_stride), rows(a.k, a.k_row_stride, a.k_head_stride),
+                     rows(a.v, a.v_row_stride, a.v_head_stride), lanes, 1.0 / a.c.D, 0, 1};
+  if (dtype == INT4DQ_ROWS_F32) return launch_type<INT4DQ_ROWS_F32>(a, p, dtype, stream);
+  if (dtype == INT4DQ_ROWS_F16) return launch_type<INT4DQ_ROWS_F16>(a, p, dtype, stream);
+  return launch_type<INT4DQ_ROWS_BF16>(a, p, dtype, stream);
 }
 
 }  // namespace int4dq

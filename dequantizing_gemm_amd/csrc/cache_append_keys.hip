@@ -1,0 +1,120 @@
+// cache_append_keys.hip -- prompts' keys, normalised and rotated, and values on their way
+// into the 4-bit cache (include/int4dq_cache_step.h), in the write kernel's
+// arrangement: four threads a token, so that the norm's factor, a group's extremes and
+// the places are found once for 8 C channels a thread, and both channels of a pair are
+// in one thread. (The mathematics is in cache_append.hip.)
+#include "cache_append.h"
+#include "cache_write.h"
+
+namespace int4dq {
+
+namespace {
+
+// Normalised and rotated channels of a thread; 0 from head_dim on. Weights, cosines and
+// sines lie 16-byte aligned, head_dim and half are multiples of 8.
+template <int DT, int C>
+__device__ __forceinline__ void transform_key(const AppendArgs& a, const AppendPlan& p, const Channels<DT, C>& x, int64_t pos,
+                                              int lane4, float y[C][8]) {
+#pragma clang fp contract(off)
+  const int D = a.c.D, half = a.half;
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[i][e] = value_of<DT>(x.raw[i][e]);
+  if (a.k_norm) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)y[i][e], (double)y[i][e], sum);
+    const float r = norm_factor(lanes_sum<4>(sum) * p.mean + a.eps);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int d = 32 * i + 8 * lane4;
+      const float4_t* const w4 = reinterpret_cast<const float4_t*>(a.k_norm + (d < D ? d : 0));
+      const float4_t w0 = w4[0], w1 = w4[1];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[i][e] = (y[i][e] * r) * (e < 4 ? w0[e % 4] : w1[e % 4]);
+    }
+  }
+  if (!a.rope) return;
+  const float* const cosines = a.rope + pos * a.rope_stride;
+  if (a.interleaved) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int d = 32 * i + 8 * lane4;
+      const bool turn = d < 2 * half;
+      const int at = turn ? d / 2 : 0;
+      const float4_t c = *reinterpret_cast<const float4_t*>(cosines + at);
+      const float4_t s = *reinterpret_cast<const float4_t*>(cosines + half + at);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float u = y[i][e], v = y[i][e + 1], ce = c[e / 2], se = s[e / 2];
+        const float u0 = u * ce, u1 = v * se, v0 = v * ce, v1 = u * se;
+        const float left = u0 - u1, right = v0 + v1;
+        y[i][e] = turn ? left : u;
+        y[i][e + 1] = turn ? right : v;
+      }
+    }
+  } else if constexpr (C % 2 == 0) {                 // all channels, in halves of 16 C
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      const int d = 32 * i + 8 * lane4;
+      const float4_t* const c4 = reinterpret_cast<const float4_t*>(cosines + d);
+      const float4_t* const s4 = reinterpret_cast<const float4_t*>(cosines + half + d);
+      const float4_t c0 = c4[0], c1 = c4[1], s0 = s4[0], s1 = s4[1];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float u = y[i][e], v = y[i + C / 2][e], ce = e < 4 ? c0[e % 4] : c1[e % 4], se = e < 4 ? s0[e % 4] : s1[e % 4];
+        const float u0 = u * ce, u1 = v * se, v0 = v * ce, v1 = u * se;
+        y[i][e] = u0 - u1;
+        y[i + C / 2][e] = v0 + v1;
+      }
+    }
+  }
+}
+
+template <int DT, int C, bool AFF>
+__global__ __launch_bounds__(256) void cache_append_quads_kernel(AppendArgs a, AppendPlan p) {
+  const int head = blockIdx.y;
+  const bool is_keys = blockIdx.z == 1;
+  write_step<C, AFF>(a.c, a.r, blockIdx.x, head, is_keys, [&](int64_t pos) { return position_there(a, pos); },
+                     [&](int64_t row, int64_t pos, int lane4, bool there) {
+                       const RowArray& in = is_keys ? p.k : p.v;
+                       Channels<DT, C> x;
+                       x.load(a.c, at_row<DT>(in, row, head), in.wide, lane4, there);
+                       if (!is_keys) return quantise<C, AFF>(a.c, lane4, [&](int i, int e) { return value_of<DT>(x.raw[i][e]); });
+                       float y[C][8];
+                       transform_key<DT, C>(a, p, x, there ? pos : 0, lane4, y);
+                       return quantise<C, AFF>(a.c, lane4, [&](int i, int e) { return y[i][e]; });
+                     });
+}
+
+template <int DT, int C>
+void launch_width(const AppendArgs& a, const AppendPlan& p, bool keys, hipStream_t stream) {
+  const dim3 grid((unsigned)store_units(a.r), (unsigned)a.c.heads, keys ? 2 : 1), block(256);
+  if (a.c.k_zeros) hipLaunchKernelGGL((cache_append_quads_kernel<DT, C, true>), grid, block, 0, stream, a, p);
+  else hipLaunchKernelGGL((cache_append_quads_kernel<DT, C, false>), grid, block, 0, stream, a, p);
+}
+
+template <int DT>
+void launch_type(const AppendArgs& a, const AppendPlan& p, bool keys, hipStream_t stream) {
+  switch (a.c.C) {
+    case 2: return launch_width<DT, 2>(a, p, keys, stream);
+    case 3: return launch_width<DT, 3>(a, p, keys, stream);
+    case 4: return launch_width<DT, 4>(a, p, keys, stream);
+    case 6: return launch_width<DT, 6>(a, p, keys, stream);
+    default: return launch_width<DT, 8>(a, p, keys, stream);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_cache_append_quads(const AppendArgs& a, const AppendPlan& p, int dtype, bool keys, hipStream_t stream) {
+  if (dtype == INT4DQ_ROWS_F32) launch_type<INT4DQ_ROWS_F32>(a, p, keys, stream);
+  else if (dtype == INT4DQ_ROWS_F16) launch_type<INT4DQ_ROWS_F16>(a, p, keys, stream);
+  else launch_type<INT4DQ_ROWS_BF16>(a, p, keys, stream);
+  return hipGetLastError();
+}
+
+}  // namespace int4dq
