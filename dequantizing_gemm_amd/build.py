@@ -42,7 +42,7 @@ ATTENTION_WIDTHS = [f"cache_attention_{more}{n}.hip" for n in (256, 128, 192, 96
 SOURCES = ["api.cpp", "quantize.hip", "unpack.hip", "dequantize.hip", "matmul_generic.hip",
            "matmul_skinny.hip", "matmul_tiled.hip", "matmul_gemv.hip", "cache_api.cpp", "cache_store.hip",
            "cache_attention.hip", "cache_attention_shared.hip", "cache_step_api.cpp", "cache_pages.hip",
-           "cache_append.hip", "cache_append_keys.hip", *ATTENTION_WIDTHS]
+           "cache_append.hip", "cache_append_prompts.hip", *ATTENTION_WIDTHS]
 
 # The gemv kernels read their MFMA accumulators with VALU ops; selecting the
 # VGPR form of the MFMA instructions keeps the accumulators in VGPRs instead of

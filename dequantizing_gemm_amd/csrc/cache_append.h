@@ -13,8 +13,8 @@ struct AppendPlan {
   RowArray q, k, v;
   int group_lanes;           // lanes of a scale's group: 4, 8, 16 or 32
   double mean;               // 1 / head_dim
-  int64_t key_blocks;        // prompts: the first blocks, where keys are among them; the others take queries
-  int heads_per_block;       // query heads that a block takes in turn
+  int heads_per_block;       // prompts: query heads that a block takes in turn
+  int64_t query_blocks;
 };
 
 template <int CTRL>
@@ -55,11 +55,10 @@ __device__ __forceinline__ const Bits<DT>* at_row(const RowArray& x, int64_t row
   return static_cast<const Bits<DT>*>(x.p) + row * x.row_stride + head * x.head_stride;
 }
 
-// Values of prompts, and with `keys` keys whose pairs a thread has by itself
-// (keys_in_thread): a block for 64 positions, a head and a side.
-hipError_t launch_cache_append_quads(const AppendArgs& a, const AppendPlan& p, int dtype, bool keys, hipStream_t stream);
+// Prompts' values and, with `keys`, their keys: those whose pairs one thread has, WIDE.
 inline bool keys_in_thread(const AppendArgs& a) {
   return !a.rope || a.interleaved || (a.c.C % 2 == 0 && a.half == 16 * a.c.C);
 }
+hipError_t launch_cache_append_prompts(const AppendArgs& a, const AppendPlan& p, int dtype, bool keys, hipStream_t stream);
 
 }  // namespace int4dq

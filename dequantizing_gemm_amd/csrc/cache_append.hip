@@ -17,6 +17,8 @@ namespace int4dq {
 
 namespace {
 
+// ---------------------------------------------------------------- 8 channels a lane
+
 // The weights, cosines and sines of 8 channels from d on, and where their partners
 // lie. WIDE, here and below: the rows' 8 channels lie 16-byte aligned in every array,
 // weights, cosines and sines as well, head_dim and half are multiples of 8, so that the
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(256) void cache_append_rows_kernel(AppendArgs a, Ap
 
 // ---------------------------------------------------------------- prompts
 
-// Keys whose pairs lie in two threads of cache_append_keys.hip: 64 positions of a
+// Keys whose pairs lie in two threads of cache_append_prompts.hip: 64 positions of a
 // sequence (find_store_block), one head, L lanes a row.
 template <int DT, int L, bool WIDE>
 __device__ __forceinline__ void append_keys(const AppendArgs& a, const AppendPlan& p, int64_t block) {
@@ -404,11 +406,12 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const Append
   }
 }
 
+// The queries, and behind them the keys that cache_append_prompts.hip leaves.
 template <int DT, int L, bool WIDE>
 __global__ __launch_bounds__(256) void cache_append_steps_kernel(AppendArgs a, AppendPlan p) {
   const int64_t block = blockIdx.x;
-  if (block < p.key_blocks) append_keys<DT, L, WIDE>(a, p, block);
-  else append_queries<DT, L, WIDE>(a, p, block - p.key_blocks);
+  if (block < p.query_blocks) append_queries<DT, L, WIDE>(a, p, block);
+  else append_keys<DT, L, WIDE>(a, p, block - p.query_blocks);
 }
 
 // ---------------------------------------------------------------- launches
@@ -422,16 +425,16 @@ hipError_t launch_lanes(const AppendArgs& a, AppendPlan p, int dtype, hipStream_
                        stream, a, p);
     return hipGetLastError();
   }
-  const bool keys = keys_in_thread(a) && WIDE;
-  const hipError_t e = launch_cache_append_quads(a, p, dtype, keys, stream);
+  const bool keys = WIDE && keys_in_thread(a);
+  const hipError_t e = launch_cache_append_prompts(a, p, dtype, keys, stream);
   if (e != hipSuccess) return e;
   // Several heads a block, which share cosines and sines, as long as that leaves twice
   // the 2048 blocks that the GPU holds at once.
   const int64_t row_blocks = (a.r.rows + ROWS - 1) / ROWS;
   p.heads_per_block = 1;
   while (p.heads_per_block < 8 && row_blocks * (a.q_heads / (2 * p.heads_per_block)) >= 4096) p.heads_per_block *= 2;
-  p.key_blocks = keys ? 0 : store_units(a.r) * a.c.heads;
-  const int64_t blocks = p.key_blocks + row_blocks * ((a.q_heads + p.heads_per_block - 1) / p.heads_per_block);
+  p.query_blocks = row_blocks * ((a.q_heads + p.heads_per_block - 1) / p.heads_per_block);
+  const int64_t blocks = p.query_blocks + (keys ? 0 : store_units(a.r) * a.c.heads);
   hipLaunchKernelGGL((cache_append_steps_kernel<DT, L, WIDE>), dim3((unsigned)blocks), dim3(256), 0, stream, a, p);
   return hipGetLastError();
 }
@@ -462,7 +465,7 @@ hipError_t launch_cache_append(const AppendArgs& a, int dtype, hipStream_t strea
   };
   const int lanes = a.c.G > 1 ? a.c.group / 8 : a.c.C <= 2 ? 8 : a.c.C <= 4 ? 16 : 32;
   const AppendPlan p{rows(a.q, a.q_row_stride, a.q_head_stride), rows(a.k, a.k_row_stride, a.k_head_stride),
-                     rows(a.v, a.v_row_stride, a.v_head_stride), lanes, 1.0 / a.c.D, 0, 1};
+                     rows(a.v, a.v_row_stride, a.v_head_stride), lanes, 1.0 / a.c.D, 1, 0};
   if (dtype == INT4DQ_ROWS_F32) return launch_type<INT4DQ_ROWS_F32>(a, p, dtype, stream);
   if (dtype == INT4DQ_ROWS_F16) return launch_type<INT4DQ_ROWS_F16>(a, p, dtype, stream);
   return launch_type<INT4DQ_ROWS_BF16>(a, p, dtype, stream);

@@ -1,4 +1,4 @@
-// cache_append_keys.hip -- prompts' keys, normalised and rotated, and values on their way
+// cache_append_prompts.hip -- prompts' keys, normalised and rotated, and values on their way
 // into the 4-bit cache (include/int4dq_cache_step.h), in the write kernel's
 // arrangement: four threads a token, so that the norm's factor, a group's extremes and
 // the places are found once for 8 C channels a thread, and both channels of a pair are
@@ -17,6 +17,21 @@ __device__ __forceinline__ void transform_key(const AppendArgs& a, const AppendP
                                               int lane4, float y[C][8]) {
 #pragma clang fp contract(off)
   const int D = a.c.D, half = a.half;
+  // Cosines and sines are asked for first, to come while the norm is summed. Halves: of
+  // the pairs of blocks i and i + C / 2; interleaved: of block i's four pairs.
+  constexpr int H = C / 2;
+  float4_t c[C], s[C];
+  const bool halves = C % 2 == 0 && !a.interleaved;
+  if (a.rope) {
+    const float* const row = a.rope + pos * a.rope_stride;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int d = 32 * (halves ? i / 2 : i) + 8 * lane4;
+      const int at = halves ? d + 4 * (i % 2) : d < 2 * half ? d / 2 : 0;
+      c[i] = *reinterpret_cast<const float4_t*>(row + at);
+      s[i] = *reinterpret_cast<const float4_t*>(row + half + at);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < C; ++i)
 #pragma unroll
@@ -38,18 +53,13 @@ __device__ __forceinline__ void transform_key(const AppendArgs& a, const AppendP
     }
   }
   if (!a.rope) return;
-  const float* const cosines = a.rope + pos * a.rope_stride;
-  if (a.interleaved) {
+  if (!halves) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int d = 32 * i + 8 * lane4;
-      const bool turn = d < 2 * half;
-      const int at = turn ? d / 2 : 0;
-      const float4_t c = *reinterpret_cast<const float4_t*>(cosines + at);
-      const float4_t s = *reinterpret_cast<const float4_t*>(cosines + half + at);
+      const bool turn = 32 * i + 8 * lane4 < 2 * half;
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const float u = y[i][e], v = y[i][e + 1], ce = c[e / 2], se = s[e / 2];
+        const float u = y[i][e], v = y[i][e + 1], ce = c[i][e / 2], se = s[i][e / 2];
         const float u0 = u * ce, u1 = v * se, v0 = v * ce, v1 = u * se;
         const float left = u0 - u1, right = v0 + v1;
         y[i][e] = turn ? left : u;
@@ -58,27 +68,20 @@ __device__ __forceinline__ void transform_key(const AppendArgs& a, const AppendP
     }
   } else if constexpr (C % 2 == 0) {                 // all channels, in halves of 16 C
 #pragma unroll
-    for (int i = 0; i < C / 2; ++i) {
-      const int d = 32 * i + 8 * lane4;
-      const float4_t* const c4 = reinterpret_cast<const float4_t*>(cosines + d);
-      const float4_t* const s4 = reinterpret_cast<const float4_t*>(cosines + half + d);
-      const float4_t c0 = c4[0], c1 = c4[1], s0 = s4[0], s1 = s4[1];
+    for (int i = 0; i < H; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float u = y[i][e], v = y[i + C / 2][e], ce = e < 4 ? c0[e % 4] : c1[e % 4], se = e < 4 ? s0[e % 4] : s1[e % 4];
+        const float u = y[i][e], v = y[i + H][e], ce = c[2 * i + e / 4][e % 4], se = s[2 * i + e / 4][e % 4];
         const float u0 = u * ce, u1 = v * se, v0 = v * ce, v1 = u * se;
         y[i][e] = u0 - u1;
-        y[i + C / 2][e] = v0 + v1;
+        y[i + H][e] = v0 + v1;
       }
-    }
   }
 }
 
 template <int DT, int C, bool AFF>
-__global__ __launch_bounds__(256) void cache_append_quads_kernel(AppendArgs a, AppendPlan p) {
-  const int head = blockIdx.y;
-  const bool is_keys = blockIdx.z == 1;
-  write_step<C, AFF>(a.c, a.r, blockIdx.x, head, is_keys, [&](int64_t pos) { return position_there(a, pos); },
+__device__ __forceinline__ void append_step(const AppendArgs& a, const AppendPlan& p, int block, int head, bool is_keys) {
+  write_step<C, AFF>(a.c, a.r, block, head, is_keys, [&](int64_t pos) { return position_there(a, pos); },
                      [&](int64_t row, int64_t pos, int lane4, bool there) {
                        const RowArray& in = is_keys ? p.k : p.v;
                        Channels<DT, C> x;
@@ -90,11 +93,32 @@ __global__ __launch_bounds__(256) void cache_append_quads_kernel(AppendArgs a, A
                      });
 }
 
+// A row's heads and sides lie side by side in one projection's output, and are read
+// together by blocks next to each other.
+template <int DT, int C, bool AFF>
+__global__ __launch_bounds__(256) void cache_append_prompts_kernel(AppendArgs a, AppendPlan p) {
+  const int which = blockIdx.x % (2 * a.c.heads), head = which % a.c.heads;
+  append_step<DT, C, AFF>(a, p, blockIdx.x / (2 * a.c.heads), head, which < a.c.heads);
+}
+
+template <int DT, int C, bool AFF>
+__global__ __launch_bounds__(256) void cache_append_values_kernel(AppendArgs a, AppendPlan p) {
+  append_step<DT, C, AFF>(a, p, blockIdx.x / a.c.heads, blockIdx.x % a.c.heads, false);
+}
+
+template <int DT, int C, bool AFF>
+void launch_form(const AppendArgs& a, const AppendPlan& p, bool keys, hipStream_t stream) {
+  const int64_t blocks = store_units(a.r) * a.c.heads;
+  if (keys)
+    hipLaunchKernelGGL((cache_append_prompts_kernel<DT, C, AFF>), dim3((unsigned)(2 * blocks)), dim3(256), 0, stream, a, p);
+  else
+    hipLaunchKernelGGL((cache_append_values_kernel<DT, C, AFF>), dim3((unsigned)blocks), dim3(256), 0, stream, a, p);
+}
+
 template <int DT, int C>
 void launch_width(const AppendArgs& a, const AppendPlan& p, bool keys, hipStream_t stream) {
-  const dim3 grid((unsigned)store_units(a.r), (unsigned)a.c.heads, keys ? 2 : 1), block(256);
-  if (a.c.k_zeros) hipLaunchKernelGGL((cache_append_quads_kernel<DT, C, true>), grid, block, 0, stream, a, p);
-  else hipLaunchKernelGGL((cache_append_quads_kernel<DT, C, false>), grid, block, 0, stream, a, p);
+  if (a.c.k_zeros) launch_form<DT, C, true>(a, p, keys, stream);
+  else launch_form<DT, C, false>(a, p, keys, stream);
 }
 
 template <int DT>
@@ -110,7 +134,7 @@ void launch_type(const AppendArgs& a, const AppendPlan& p, bool keys, hipStream_
 
 }  // namespace
 
-hipError_t launch_cache_append_quads(const AppendArgs& a, const AppendPlan& p, int dtype, bool keys, hipStream_t stream) {
+hipError_t launch_cache_append_prompts(const AppendArgs& a, const AppendPlan& p, int dtype, bool keys, hipStream_t stream) {
   if (dtype == INT4DQ_ROWS_F32) launch_type<INT4DQ_ROWS_F32>(a, p, keys, stream);
   else if (dtype == INT4DQ_ROWS_F16) launch_type<INT4DQ_ROWS_F16>(a, p, keys, stream);
   else launch_type<INT4DQ_ROWS_BF16>(a, p, keys, stream);

@@ -1,7 +1,7 @@
 // cache_write.h -- 64 positions of a sequence written into the 4-bit cache: the
 // codes of one token's channels, four threads a token, and how they leave. Shared by
 // the kernel that writes rows as they are (cache_store.hip) and the one that normalises
-// and rotates keys on the way (cache_append_keys.hip).
+// and rotates keys on the way (cache_append_prompts.hip).
 #pragma once
 
 #include "cache_rows.h"
