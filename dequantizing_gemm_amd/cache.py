@@ -252,9 +252,9 @@ def int4_cache_read(cache: Int4Cache, page_table: torch.Tensor, lengths: torch.T
     return out
 
 
-def _workspace_bytes(cache, plan, q_heads, shares=False):
+def _workspace_bytes(cache, plan, q_heads, shares=False, share_from=-1):
     if shares:
-        n = lib.int4_cache_attention_ex_workspace_bytes(cache._ref, ctypes.addressof(plan), q_heads, 1)
+        n = lib.int4_cache_attention_ex_workspace_bytes(cache._ref, ctypes.addressof(plan), q_heads, 1, share_from)
     else:
         n = lib.int4_cache_attention_workspace_bytes(cache._ref, ctypes.addressof(plan), q_heads)
     if n < 0:
@@ -262,27 +262,38 @@ def _workspace_bytes(cache, plan, q_heads, shares=False):
     return n
 
 
-def cache_attention_workspace_bytes(cache: Int4Cache, batch: int, rows: int, q_heads: int, shared: bool = False) -> int:
+def _share_from(n):
+    if n is None:
+        return -1
+    if n < 0:
+        raise ValueError(f"share_from must be >= 0 (got {n})")
+    return int(n)
+
+
+def cache_attention_workspace_bytes(cache: Int4Cache, batch: int, rows: int, q_heads: int, shared: bool = False,
+                                    share_from: int | None = None) -> int:
     """Bytes of workspace int4_cache_attention uses for these sizes: ``rows`` rows
     of ``q_heads`` query heads over ``batch`` sequences, whatever their page tables
     (a call whose table is short takes less, or none); with ``shared`` of calls that
-    are given shared tokens too."""
+    are given shared tokens too (and ``share_from``)."""
     _is_cache(cache)
     one = None if rows == batch else 1
     most = 2 ** 31 - 1
-    return _workspace_bytes(cache, _RowsStruct(None, most, most, None, one, batch, rows), q_heads, shared)
+    return _workspace_bytes(cache, _RowsStruct(None, most, most, None, one, batch, rows), q_heads, shared, _share_from(share_from))
 
 
-def cache_attention_workspace(cache: Int4Cache, batch: int, rows: int, q_heads: int, shared: bool = False) -> torch.Tensor:
+def cache_attention_workspace(cache: Int4Cache, batch: int, rows: int, q_heads: int, shared: bool = False,
+                              share_from: int | None = None) -> torch.Tensor:
     """A workspace tensor for int4_cache_attention(..., workspace=)."""
-    return torch.empty(cache_attention_workspace_bytes(cache, batch, rows, q_heads, shared), dtype=torch.uint8,
+    return torch.empty(cache_attention_workspace_bytes(cache, batch, rows, q_heads, shared, share_from), dtype=torch.uint8,
                        device=cache.device)
 
 
 def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Tensor, lengths: torch.Tensor,
                          starts: torch.Tensor | None = None, *, scale: float | None = None, causal: bool = True,
                          window: int = 0, return_lse: bool = False, out: torch.Tensor | None = None,
-                         workspace: torch.Tensor | None = None, sinks: int = 0, shared: torch.Tensor | None = None):
+                         workspace: torch.Tensor | None = None, sinks: int = 0, shared: torch.Tensor | None = None,
+                         share_from: int | None = None):
     """Softmax attention of q [rows, q_heads, head_dim] (float16 or bfloat16, any
     row and head strides) over the cache: out of q's shape and dtype, and with
     ``return_lse`` the logarithm of each softmax sum, float32 [rows, q_heads].
@@ -297,8 +308,9 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
 
     ``sinks``: with a window, the first ``sinks`` tokens stay visible too. ``shared``
     int32 [1] on the GPU: all sequences begin with the same shared[0] tokens, which
-    are then read once for many sequences with few rows each, through the first row
-    of ``page_table``; the result is what it is without."""
+    are then read once for all of them where that pays (or from ``share_from`` tokens
+    on), through the first row of ``page_table``; the result is what it is without, but
+    for rounding."""
     _is_cache(cache)
     q_heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
     qs = _rows_array(cache, q, "q", q_heads)
@@ -320,7 +332,7 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
         if shared.shape[0] != 1:
             raise ValueError(f"shared must have one entry (got {shared.shape[0]})")
     if workspace is None:
-        n = _workspace_bytes(cache, plan, q_heads, shared is not None)
+        n = _workspace_bytes(cache, plan, q_heads, shared is not None, _share_from(share_from))
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     else:
@@ -333,7 +345,7 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
     to = (out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr() if n else None, n)
     if sinks or shared is not None:
         _call(cache, lib.int4_cache_attention_ex, "int4_cache_attention", *args, int(sinks),
-              None if shared is None else shared.data_ptr(), *to)
+              None if shared is None else shared.data_ptr(), _share_from(share_from), *to)
     else:
         _call(cache, lib.int4_cache_attention, "int4_cache_attention", *args, *to)
     return (out, lse) if return_lse else out

@@ -44,9 +44,9 @@ CACHE_STEP_SIGNATURES = {
     "int4_cache_release": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "int4_cache_extend": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
     "int4_cache_append": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp, _vp]),
-    "int4_cache_attention_ex": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _i64, ctypes.c_float, _int, _i64, _i64, _vp, _vp,
-                                       _vp, _vp, _i64, _vp]),
-    "int4_cache_attention_ex_workspace_bytes": (_i64, [_vp, _vp, _i64, _int]),
+    "int4_cache_attention_ex": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _i64, ctypes.c_float, _int, _i64, _i64, _vp, _i64,
+                                       _vp, _vp, _vp, _i64, _vp]),
+    "int4_cache_attention_ex_workspace_bytes": (_i64, [_vp, _vp, _i64, _int, _i64]),
 }
 for _name, (_res, _args) in CACHE_STEP_SIGNATURES.items():
     _fn = getattr(lib, _name)

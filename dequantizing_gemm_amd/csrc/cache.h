@@ -149,6 +149,7 @@ struct AttentionArgs {
   // as one, and each sequence's own tokens behind them.
   int part;                 // kWhole, kOwnPart or kSharedPart
   const int32_t* shared;    // the number of shared tokens (parts)
+  int least_shared;         // fewer are left to the sequences
   int all;                  // kSharedPart: the sequences of the batch; r.batch is 1
 };
 constexpr int kWhole = 0, kOwnPart = 1, kSharedPart = 2;

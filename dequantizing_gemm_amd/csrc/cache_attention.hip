@@ -15,6 +15,7 @@ __global__ __launch_bounds__(1024) void cache_attention_plan_kernel(AttentionArg
   __shared__ float works[2][16];
   __shared__ int longest[16], adds[2][16];
   __shared__ PlanEntry sums[2][16];
+  const bool parts = sched.partial && leaves_parts(a, sched);
   const SequenceWork own = tid < a.r.batch ? sequence_work(a, sched.tile_rows, tid) : SequenceWork{};
   auto of = [&](int b) { return b == tid ? own : sequence_work(a, sched.tile_rows, b); };
   float work = 0.0f, tiles = 0.0f;
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(1024) void cache_attention_plan_kernel(AttentionArg
       const SequenceWork w = of(b);
       const int chunks = w.tiles > 0 ? chunks_of(w.steps, per) : 0;
       mine = chunks * w.tiles;
-      mine_slots = chunks > 1 || sched.partial ? mine : 0;
+      mine_slots = chunks > 1 || parts ? mine : 0;
     }
     int upto = lane_scan(mine), slots_upto = lane_scan(mine_slots);
     if (lane == kWave - 1) sums[turn][wave] = PlanEntry{upto, slots_upto};
@@ -183,7 +184,7 @@ template <int C>
 hipError_t launch_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream) {
   hipError_t e = s.planned ? launch_cache_attention_plan(a, s, ws, stream) : hipSuccess;
   if (e == hipSuccess)
-    e = sink_end(a) > 0 ? launch_attention_width<C, true>(a, s, ws, stream) : launch_attention_width<C, false>(a, s, ws, stream);
+    e = sink_end(a) > 0 ? launch_attention_width<C, true>(a, s, ws, {}, stream) : launch_attention_width<C, false>(a, s, ws, {}, stream);
   if (e != hipSuccess || s.target == 0) return e;
   const unsigned rows = (unsigned)(a.r.starts || a.ratio > 4 ? 4 : a.ratio);
   hipLaunchKernelGGL(cache_attention_join_kernel<C>, dim3((unsigned)(workspace_slots(s) * a.c.heads), rows), dim3(256),
@@ -194,25 +195,25 @@ hipError_t launch_width(const AttentionArgs& a, const Schedule& s, const Workspa
 }  // namespace
 
 extern template hipError_t launch_attention_width<2, false>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<false>&, hipStream_t);
 extern template hipError_t launch_attention_width<2, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<3, false>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<false>&, hipStream_t);
 extern template hipError_t launch_attention_width<3, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<4, false>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<false>&, hipStream_t);
 extern template hipError_t launch_attention_width<4, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<6, false>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<false>&, hipStream_t);
 extern template hipError_t launch_attention_width<6, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<8, false>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<false>&, hipStream_t);
 extern template hipError_t launch_attention_width<8, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                           hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 
 int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int ratio) {
   const Schedule s = plan_of(c, r, ratio);
@@ -220,7 +221,14 @@ int64_t cache_attention_workspace(const CacheView& c, const RowsView& r, int rat
 }
 
 hipError_t launch_cache_attention(const AttentionArgs& a, void* workspace, int64_t bytes, hipStream_t stream) {
-  Schedule s = plan_of(a.c, a.r, a.ratio);
+  const int tile_rows = tile_rows_of(a.c, a.r, a.ratio);
+  // With a window and first tokens few blocks are busy where there are few tiles, and
+  // prompts' tiles are short: blocks of 8 steps. One sequence, window 8192, 64 first
+  // tokens, groups of 32 with zero points, 24.0 -> 18.9 us; window 1000 20.1 -> 17.5; 4
+  // prompts in chunks, window 1500, 142 -> 137; but 8 sequences of one row each 15.5 -> 16.4,
+  // of 3 to 5 rows 20.2 -> 22.8.
+  const bool few = a.r.batch <= 4 && a.r.rows * a.ratio <= 4 * tile_rows;
+  Schedule s = plan_for(a.c, a.r, a.ratio, tile_rows, sink_end(a) > 0 && (few || tile_rows == kWideRows) ? 8 : 16);
   auto fits = [&] { return s.target == 0 || bytes >= workspace_bytes(s, a.c.heads, a.c.C, a.r.batch); };
   if (s.crowded && !fits()) {            // a workspace made for a larger call may have room for fewer cuts
     s.units -= s.target;

@@ -668,14 +668,14 @@ __device__ __forceinline__ void load_value_scales(const CacheView& c, int unit, 
 
 // What a block does first: its share, the record of a partial result, the number
 // of them. False if it has no share.
-__device__ __forceinline__ bool begin_block(const AttentionArgs& a, const Schedule& sched, const Workspace& ws,
+__device__ __forceinline__ bool begin_block(const AttentionArgs& a, const Schedule& sched, const Workspace& ws, int block,
                                             BlockWork* work) {
   const int heads = a.c.heads;
   int used;
-  const bool found = find_block(a, sched, ws, blockIdx.x / heads, work, &used);
-  if (sched.target > 0 && !sched.planned && blockIdx.x == 0 && threadIdx.x == 0) *ws.used = used;
+  const bool found = find_block(a, sched, ws, block / heads, work, &used);
+  if (sched.target > 0 && !sched.planned && block == 0 && threadIdx.x == 0) *ws.used = used;
   if (!found) return false;
-  if ((work->chunks > 1 || sched.partial) && blockIdx.x % heads == 0 && threadIdx.x == 0)
+  if ((work->chunks > 1 || sched.partial) && block % heads == 0 && threadIdx.x == 0)
     ws.record[work->slot] = PartRecord{work->w.first, work->tile * sched.tile_rows, work->w.rows * a.ratio, work->chunk,
                                        work->chunks, {}};
   return true;
@@ -719,12 +719,36 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // parts of a batch that shares tokens. What other calls run has none of that in it: as
 // one form the registers of both would not do (up to 10 more, and spills where tiles
 // fill them).
+//
+// A second share of blocks in a launch, of the shared part: those from `from` on.
 template <bool MORE>
-__device__ __forceinline__ void only_whole(AttentionArgs* a, Schedule* s) {
-  if constexpr (!MORE) {
+struct Second {};
+template <>
+struct Second<true> {
+  unsigned from;                         // 0: there is none
+  Schedule sched;
+  Workspace ws;
+};
+
+// What the block is part of, and its number there.
+template <bool MORE>
+__device__ __forceinline__ int block_of(AttentionArgs* a, Schedule* s, Workspace* ws, const Second<MORE>& second) {
+  if constexpr (MORE) {
+    if (second.from == 0 || blockIdx.x < second.from) {
+      s->partial = leaves_parts(*a, *s);
+      return blockIdx.x;
+    }
+    a->part = kSharedPart;
+    a->all = a->r.batch;
+    a->r.batch = 1;
+    *s = second.sched;
+    *ws = second.ws;
+    return blockIdx.x - second.from;
+  } else {
     a->sinks = 0;
     a->part = kWhole;
     s->partial = 0;
+    return blockIdx.x;
   }
 }
 
@@ -735,14 +759,14 @@ __device__ __forceinline__ void only_whole(AttentionArgs* a, Schedule* s) {
 // are joined through LDS.
 template <int C, int GC, int QT, bool AFF, bool MORE>
 __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void cache_attention_kernel(
-    AttentionArgs a, Schedule sched, Workspace ws) {
+    AttentionArgs a, Schedule sched, Workspace ws, Second<MORE> second) {
   constexpr int NG = C / GC, DB = 16 * C, TR = 16 * QT;
-  only_whole<MORE>(&a, &sched);
+  const int block = block_of<MORE>(&a, &sched, &ws, second);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
-  const int heads = a.c.heads, kh = blockIdx.x % heads;
+  const int heads = a.c.heads, kh = block % heads;
   BlockWork work;
-  if (!begin_block(a, sched, ws, &work)) return;
+  if (!begin_block(a, sched, ws, block, &work)) return;
   Rows<C, GC, QT, AFF> r;
   r.row = lane & 15;
   r.quarter = lane >> 4;
@@ -912,15 +936,16 @@ __global__ __launch_bounds__(256, resident_blocks(C, C / GC, AFF, 16 * QT)) void
 // those in LDS, in the lanes' order, for all, one step ahead of their use (two
 // buffers, one barrier a step).
 template <int C, int GC, int QT, bool AFF, bool MORE>
-__global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(AttentionArgs a, Schedule sched, Workspace ws) {
+__global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(AttentionArgs a, Schedule sched, Workspace ws,
+                                                                        Second<MORE> second) {
   constexpr int NG = C / GC, DB = 16 * C, TR = kWideRows;
-  only_whole<MORE>(&a, &sched);
+  const int block = block_of<MORE>(&a, &sched, &ws, second);
   constexpr int VJ = (C + 3) / 4;        // byte rows (of 16) of the values that a wavefront prepares
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);     // known to be uniform
-  const int heads = a.c.heads, kh = blockIdx.x % heads;
+  const int heads = a.c.heads, kh = block % heads;
   BlockWork work;
-  if (!begin_block(a, sched, ws, &work)) return;
+  if (!begin_block(a, sched, ws, block, &work)) return;
   Rows<C, GC, QT, AFF> r;
   r.row = lane & 15;
   r.quarter = lane >> 4;
@@ -1108,8 +1133,9 @@ __global__ __launch_bounds__(512 / QT) void cache_attention_wide_kernel(Attentio
 hipError_t launch_cache_attention_plan(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream);
 
 // Defined for each width in a file of its own: launches the form for the cache's
-// groups and the schedule's tile height. MORE: see only_whole.
+// groups and the schedule's tile height, with a second share of as high tiles behind it.
 template <int C, bool MORE>
-hipError_t launch_attention_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws, hipStream_t stream);
+hipError_t launch_attention_width(const AttentionArgs& a, const Schedule& s, const Workspace& ws,
+                                  const Second<MORE>& second, hipStream_t stream);
 
 }  // namespace int4dq

@@ -3,5 +3,6 @@
 #include "cache_attention_launch.h"
 
 namespace int4dq {
-template hipError_t launch_attention_width<6, true>(const AttentionArgs&, const Schedule&, const Workspace&, hipStream_t);
+template hipError_t launch_attention_width<6, true>(const AttentionArgs&, const Schedule&, const Workspace&,
+                                                    const Second<true>&, hipStream_t);
 }

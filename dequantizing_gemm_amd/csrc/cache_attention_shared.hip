@@ -20,15 +20,49 @@ namespace {
 struct Parts {
   Schedule own, shared;
   int64_t own_bytes, shared_bytes;
+  int from;                  // shared tokens, at least
 };
 
-// False: sharing would not pay, or cannot be.
-bool plan_parts(const CacheView& c, const RowsView& r, int ratio, Parts* p) {
-  if (r.batch < 2) return false;
+// From how many shared tokens on sharing pays; 0: never. Measured, 8 x 4 heads of 128,
+// shared against not.
+//  - Few rows, tiles of 16 at most half filled by a sequence: 200 own tokens, 4 sequences
+//    18 and 21 us with 8192 shared tokens, 16 and 15 with 1984; 16 sequences 24 and 32,
+//    18 and 19; 64 sequences 44 and 88, 32 and 32, with 512 30 and 16; 2 sequences, 18 and
+//    17.5, with 32768 tokens 30 and 27.5.
+//  - More rows take codes apart as often either way; what is saved is what the
+//    sequences' last tiles leave empty, which has to pay for the join: 16 sequences
+//    of 30 to 250 rows 850 and 1040 us with 20011 shared tokens (64 tiles and 72),
+//    519 and 510 with 8192; 16 of 16 to 64 rows 330 and 368, 182 and 177; but 4 of 30 to 250
+//    rows 434 and 417, 16 of 100 to 500 2108 and 1999, 16 of 4 rows each, whose tiles are
+//    full, 68 and 58.
+int64_t sharing_pays(const RowsView& r, int ratio) {
+  const int64_t rows = r.rows * ratio, tokens = 24576 / (r.batch > 0 ? r.batch : 1);
+  if (rows <= 8 * (int64_t)r.batch) return r.batch < 4 ? 0 : tokens > 1536 ? tokens : 1536;
+  return r.batch >= 8 && rows > 64 * (int64_t)r.batch && rows <= 640 * (int64_t)r.batch && rows <= 16384 ? 16384 : 0;
+}
+
+// The tiles of the shared part. Measured with the sequences' own in tiles of 16 rows,
+// tiles of 16 (in one launch), 32 and 128 rows: 64 rows 24, 29 and 40 us with 8192 shared
+// tokens, 45, 47 and 59 with 32768; 256 rows 44, 43 and 49, 104, 92 and 92; 512 rows 71, 67
+// and 71, 198, 169 and 162; 1024 rows 78, 72 and 77 with 1984.
+int shared_tile_rows(const CacheView& c, int64_t rows) {
+  const int groups = c.C / scale_blocks(c), most = 16 * max_tiles(c.C, groups, c.affine);
+  if (rows > 1024 && wide_tiles(c.C, groups, c.affine) > 0) return kWideRows;
+  return rows > 128 ? most : 16;
+}
+
+// False: sharing would not pay, or cannot be. from < 0: where it pays.
+bool plan_parts(const CacheView& c, const RowsView& r, int ratio, int64_t from, Parts* p) {
+  if (from < 0) from = sharing_pays(r, ratio);
+  else if (from == 0) from = 1;
+  if (from == 0 || (r.max_pages << c.page_shift) < from) return false;
+  p->from = from < INT32_MAX ? (int)from : INT32_MAX;
   RowsView one = r;
   one.batch = 1;
-  p->own = plan_of(c, r, ratio);
-  p->shared = plan_of(c, one, ratio);
+  // A join follows in any case: blocks of 8 steps, not 16 (24 sequences' rows, 1984
+  // shared tokens: 21.1 -> 17.3 us; of 4: 16.2, but 33.1 -> 37.5 with 32768).
+  p->own = plan_for(c, r, ratio, tile_rows_of(c, r, ratio), 8);
+  p->shared = plan_for(c, one, ratio, shared_tile_rows(c, r.rows * ratio), 8);
   if (p->own.target == 0 || p->shared.target == 0) return false;
   p->own.partial = p->shared.partial = 1;
   p->own_bytes = (workspace_bytes(p->own, c.heads, c.C, r.batch) + 255) / 256 * 256;
@@ -111,13 +145,19 @@ hipError_t launch_width(const AttentionArgs& whole, const Parts& p, const Worksp
     const hipError_t e = launch_cache_attention_plan(a, p.own, ws, stream);
     if (e != hipSuccess) return e;
   }
-  hipError_t e = launch_attention_width<C, true>(a, p.own, ws, stream);
+  // one launch where tiles are as high, so that the sequences' own tokens fill in; not with
+  // the form for prompts, which fills the GPU (917 us together, 850 apart)
+  const bool together = p.own.tile_rows == p.shared.tile_rows && p.own.tile_rows != kWideRows;
+  const Second<true> second{together ? (unsigned)(p.own.units * a.c.heads) : 0, p.shared, ws2};
+  hipError_t e = launch_attention_width<C, true>(a, p.own, ws, second, stream);
   if (e != hipSuccess) return e;
-  a.part = kSharedPart;
-  a.all = a.r.batch;
-  a.r.batch = 1;
-  e = launch_attention_width<C, true>(a, p.shared, ws2, stream);
-  if (e != hipSuccess) return e;
+  if (!together) {
+    a.part = kSharedPart;
+    a.all = a.r.batch;
+    a.r.batch = 1;
+    e = launch_attention_width<C, true>(a, p.shared, ws2, {}, stream);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(cache_attention_parts_kernel<C>, dim3((unsigned)(p.own.units * whole.c.heads), (unsigned)(p.own.tile_rows / 16)),
                      dim3(256), 0, stream, whole, p.own, ws, p.shared, ws2);
   return hipGetLastError();
@@ -126,25 +166,28 @@ hipError_t launch_width(const AttentionArgs& whole, const Parts& p, const Worksp
 }  // namespace
 
 extern template hipError_t launch_attention_width<2, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                          hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<3, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                          hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<4, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                          hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<6, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                          hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 extern template hipError_t launch_attention_width<8, true>(const AttentionArgs&, const Schedule&, const Workspace&,
-                                                          hipStream_t);
+                                                    const Second<true>&, hipStream_t);
 
-int64_t cache_attention_shared_workspace(const CacheView& c, const RowsView& r, int ratio) {
+int64_t cache_attention_shared_workspace(const CacheView& c, const RowsView& r, int ratio, int64_t from) {
   Parts p;
-  return plan_parts(c, r, ratio, &p) ? p.own_bytes + p.shared_bytes : 0;
+  return plan_parts(c, r, ratio, from, &p) ? p.own_bytes + p.shared_bytes : 0;
 }
 
-hipError_t launch_cache_attention_shared(const AttentionArgs& a, void* workspace, int64_t bytes, hipStream_t stream) {
+hipError_t launch_cache_attention_shared(const AttentionArgs& args, int64_t from, void* workspace, int64_t bytes,
+                                         hipStream_t stream) {
   Parts p;
-  if (!plan_parts(a.c, a.r, a.ratio, &p) || bytes < p.own_bytes + p.shared_bytes)
-    return launch_cache_attention(a, workspace, bytes, stream);
+  if (!plan_parts(args.c, args.r, args.ratio, from, &p) || bytes < p.own_bytes + p.shared_bytes)
+    return launch_cache_attention(args, workspace, bytes, stream);
+  AttentionArgs a = args;
+  a.least_shared = p.from;
   const Workspace ws = workspace_at(workspace, p.own, a.c.heads, a.c.C);
   const Workspace ws2 = workspace_at(static_cast<uint8_t*>(workspace) + p.own_bytes, p.shared, a.c.heads, a.c.C);
   switch (a.c.C) {

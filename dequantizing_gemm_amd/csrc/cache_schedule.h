@@ -31,7 +31,7 @@ struct Schedule {
   int units;                             // blocks per key/value head
   int crowded;                           // tiles may be more than the target by up to half
   int planned;                           // the blocks of each sequence are counted by a kernel of its own
-  int partial;                           // every block leaves a partial result, whole tiles too
+  int partial;                           // every block leaves a partial result, whole tiles too, where tokens are shared
 };
 
 // From more sequences than a wavefront looks through at once, their blocks are
@@ -63,8 +63,14 @@ struct SequenceWork {
 
 // The first token of the part of the keys that a call sees, and the end of the first
 // tokens that stay visible with a window (0: none).
-__host__ __device__ inline int first_key(const AttentionArgs& a) {
-  return a.part == kOwnPart && *a.shared > 0 ? *a.shared : 0;
+__host__ __device__ inline int shared_tokens(const AttentionArgs& a) {
+  const int n = *a.shared;
+  return n > 0 && n >= a.least_shared ? n : 0;
+}
+__host__ __device__ inline int first_key(const AttentionArgs& a) { return a.part == kOwnPart ? shared_tokens(a) : 0; }
+// Whether whole tiles leave a partial result too.
+__host__ __device__ inline int leaves_parts(const AttentionArgs& a, const Schedule& s) {
+  return s.partial && shared_tokens(a) > 0;
 }
 __host__ __device__ inline int sink_end(const AttentionArgs& a) {
   return a.window <= 0 || a.sinks <= 0 ? 0 : a.sinks < INT32_MAX ? (int)a.sinks : INT32_MAX;
@@ -75,7 +81,7 @@ __host__ __device__ inline SequenceWork sequence_work(const AttentionArgs& a, in
   const bool all = a.part == kSharedPart;            // the rows of all sequences, the shared tokens' length
   const int s0 = !a.r.starts ? b : a.r.starts[b];
   w.end = a.r.starts ? a.r.starts[all ? a.all : b + 1] : all ? a.all : b + 1;
-  w.length = all ? *a.shared : a.r.lengths[b];
+  w.length = all ? shared_tokens(a) : a.r.lengths[b];
   w.first = s0 > 0 ? s0 : 0;
   const int last = w.end < a.r.rows ? w.end : (int)a.r.rows;
   w.rows = last > w.first ? last - w.first : 0;
@@ -277,12 +283,18 @@ constexpr int kComputeUnits = 256;
 // average, 8 key/value heads, few rows' form and prompts': head width 128, 128 rows
 // 39 us and 52, 256 rows 60 and 60, 512 rows 91 and 90; width 256 (tiles of 16),
 // 128 rows 69 and 71, 192 rows 96 and 90.
-inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
-  Schedule s{};
+inline int tile_rows_of(const CacheView& c, const RowsView& r, int ratio) {
   const int64_t mean = (r.rows * ratio + r.batch - 1) / r.batch;
   const int groups = c.C / scale_blocks(c), most = 16 * max_tiles(c.C, groups, c.affine);
   const bool wide = mean > most / 16 * kWideRows && wide_tiles(c.C, groups, c.affine) > 0;
-  s.tile_rows = wide ? kWideRows : mean <= 16 ? 16 : most;
+  return wide ? kWideRows : mean <= 16 ? 16 : most;
+}
+
+// The cut for tiles of that height, one of which there is a form.
+inline Schedule plan_for(const CacheView& c, const RowsView& r, int ratio, int tile_rows, int min_steps = 16) {
+  Schedule s{};
+  const int groups = c.C / scale_blocks(c);
+  s.tile_rows = tile_rows;
   const int resident = resident_blocks(c.C, groups, c.affine, s.tile_rows);
   s.target = (resident * kComputeUnits + c.heads - 1) / c.heads;
   // Four for each wavefront of the form for few rows (16 sequences of 2650 tokens, 3 to
@@ -291,7 +303,7 @@ inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   // every step: that suits many rows (8 sequences, 512 rows each: 87 us with 16, 10 and
   // 6) better than few on one sequence (400 rows on 3000 tokens 47, 37 and 35 us; 1200
   // rows on 1500 tokens 41, 36 and 40).
-  s.min_steps = 16;
+  s.min_steps = min_steps;
   // Where no sequence can have more, every tile is left to one block and the join
   // kernel's launch is saved.
   if ((r.max_pages << c.page_shift) <= s.min_steps * kStep) s.target = 0;
@@ -300,6 +312,9 @@ inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
   s.crowded = tiles > s.target && 2 * fewest <= 3 * (int64_t)s.target;
   s.units = (int)(s.target * (s.crowded ? 2 : 1) + tiles);
   return s;
+}
+inline Schedule plan_of(const CacheView& c, const RowsView& r, int ratio) {
+  return plan_for(c, r, ratio, tile_rows_of(c, r, ratio));
 }
 
 }  // namespace int4dq

@@ -62,11 +62,12 @@ hipError_t launch_cache_append(const AppendArgs& a, int dtype, hipStream_t strea
 
 // ---------------------------------------------------------------- attention over shared tokens
 
-// Attention of a batch whose sequences begin with the same a.shared tokens; without
-// sharing where that would not pay, or the workspace is too small for it.
-hipError_t launch_cache_attention_shared(const AttentionArgs& a, void* workspace, int64_t workspace_bytes,
+// Attention of a batch whose sequences begin with the same a.shared tokens, computed
+// once from `from` of them on (below 0: where that pays); each sequence for itself below,
+// and where the workspace is too small.
+hipError_t launch_cache_attention_shared(const AttentionArgs& a, int64_t from, void* workspace, int64_t workspace_bytes,
                                          hipStream_t stream);
 // 0: a call of these sizes does not share.
-int64_t cache_attention_shared_workspace(const CacheView& c, const RowsView& r, int ratio);
+int64_t cache_attention_shared_workspace(const CacheView& c, const RowsView& r, int ratio, int64_t from);
 
 }  // namespace int4dq

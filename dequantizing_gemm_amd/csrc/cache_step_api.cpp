@@ -116,7 +116,7 @@ int int4_cache_append(const int4_cache_t* cache, const int4_cache_rows_t* rows, 
 
 int int4_cache_attention_ex(const int4_cache_t* cache, const int4_cache_rows_t* rows, const void* q, int64_t q_row_stride,
                             int64_t q_head_stride, int dtype, int64_t q_heads, float scale, int causal, int64_t window,
-                            int64_t sinks, const int32_t* shared, void* out, float* lse, void* workspace,
+                            int64_t sinks, const int32_t* shared, int64_t share_from, void* out, float* lse, void* workspace,
                             int64_t workspace_bytes, void* stream) {
   const char* fn = "int4_cache_attention_ex";
   AttentionArgs a;
@@ -127,13 +127,13 @@ int int4_cache_attention_ex(const int4_cache_t* cache, const int4_cache_rows_t* 
   if (a.r.rows == 0 || a.r.batch == 0) return ok();
   a.sinks = sinks;
   a.shared = shared;
-  return hip_status(shared ? int4dq::launch_cache_attention_shared(a, workspace, workspace_bytes, (hipStream_t)stream)
+  return hip_status(shared ? int4dq::launch_cache_attention_shared(a, share_from, workspace, workspace_bytes, (hipStream_t)stream)
                            : int4dq::launch_cache_attention(a, workspace, workspace_bytes, (hipStream_t)stream),
                     "int4_cache_attention_ex launch");
 }
 
 int64_t int4_cache_attention_ex_workspace_bytes(const int4_cache_t* cache, const int4_cache_rows_t* rows, int64_t q_heads,
-                                                int shares) {
+                                                int shares, int64_t share_from) {
   const char* fn = "int4_cache_attention_ex_workspace_bytes";
   CacheView c;
   RowsView r;
@@ -145,7 +145,7 @@ int64_t int4_cache_attention_ex_workspace_bytes(const int4_cache_t* cache, const
   if (r.rows == 0 || r.batch == 0) return 0;
   const int ratio = (int)(q_heads / c.heads);
   const int64_t whole = int4dq::cache_attention_workspace(c, r, ratio);
-  const int64_t parts = shares ? int4dq::cache_attention_shared_workspace(c, r, ratio) : 0;
+  const int64_t parts = shares ? int4dq::cache_attention_shared_workspace(c, r, ratio, share_from) : 0;
   return whole > parts ? whole : parts;
 }
 

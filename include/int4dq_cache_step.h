@@ -127,10 +127,12 @@ int int4_cache_append(const int4_cache_t *cache, const int4_cache_rows_t *rows,
  *   shared  in : [1], or NULL: every sequence begins with the same shared[0] tokens
  *           (below 0: none). A sequence sees of them what it sees of its own (all
  *           up to its length, its rows up to their positions). They are read through
- *           the first row of page_table, whatever lengths[0] is, once for many
- *           sequences where that pays: with few rows a sequence, and with a workspace
- *           for it. The other entries of page_table that stand for them have to name
+ *           the first row of page_table, whatever lengths[0] is, once for all
+ *           sequences where that pays, and with a workspace for it. The other entries of page_table that stand for them have to name
  *           the same keys and values.
+ *   share_from  the least number of shared tokens that are computed once, whatever
+ *           it costs; below 0: the library chooses, by the number of sequences and of
+ *           their rows. Results may differ in rounding.
  *   The arithmetic is that of int4_cache_attention; with shared tokens the two parts
  *   of a row are joined in binary32.
  * Errors: those of int4_cache_attention, and EINVAL for sinks < 0.
@@ -138,8 +140,8 @@ int int4_cache_append(const int4_cache_t *cache, const int4_cache_rows_t *rows,
 int int4_cache_attention_ex(const int4_cache_t *cache, const int4_cache_rows_t *rows, const void *q,
                             int64_t q_row_stride, int64_t q_head_stride, int dtype, int64_t q_heads,
                             float scale, int causal, int64_t window, int64_t sinks,
-                            const int32_t *shared, void *out, float *lse, void *workspace,
-                            int64_t workspace_bytes, void *stream);
+                            const int32_t *shared, int64_t share_from, void *out, float *lse,
+                            void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * As int4_cache_attention_workspace_bytes, of int4_cache_attention_ex; shares: 0 where
@@ -147,7 +149,7 @@ int int4_cache_attention_ex(const int4_cache_t *cache, const int4_cache_rows_t *
  */
 int64_t int4_cache_attention_ex_workspace_bytes(const int4_cache_t *cache,
                                                 const int4_cache_rows_t *rows, int64_t q_heads,
-                                                int shares);
+                                                int shares, int64_t share_from);
 
 #ifdef __cplusplus
 }

@@ -36,9 +36,9 @@ hipError_t launch_cache_release(const PagesArgs&, const uint8_t*, const int32_t*
 hipError_t launch_cache_extend(const PagesArgs&, const int32_t*, int32_t*, int64_t*, int64_t, hipStream_t) { ++calls; return hipSuccess; }
 hipError_t launch_cache_append(const AppendArgs&, int, hipStream_t) { ++calls; return hipSuccess; }
 hipError_t launch_cache_attention(const AttentionArgs&, void*, int64_t, hipStream_t) { ++calls; return hipSuccess; }
-hipError_t launch_cache_attention_shared(const AttentionArgs&, void*, int64_t, hipStream_t) { ++shared_calls; return hipSuccess; }
+hipError_t launch_cache_attention_shared(const AttentionArgs&, int64_t, void*, int64_t, hipStream_t) { ++shared_calls; return hipSuccess; }
 int64_t cache_attention_workspace(const CacheView&, const RowsView&, int) { return 512; }
-int64_t cache_attention_shared_workspace(const CacheView&, const RowsView&, int) { return 1024; }
+int64_t cache_attention_shared_workspace(const CacheView&, const RowsView&, int, int64_t) { return 1024; }
 }  // namespace int4dq
 extern "C" const char* int4_last_error(void);
 
@@ -145,6 +145,7 @@ static void attention() {
     a.sinks = pick(0, 2) ? pick(0, pick(0, 1) ? 10 : 400) : pick(0, 1) ? INT64_MAX : 0;
     const int32_t shared = (int32_t)(pick(0, 4) ? pick(0, most + 100) : pick(-100, 0));
     a.shared = &shared;
+    a.least_shared = (int)pick(0, 1) * (int)pick(0, 500);
     // what each row sees, by the definition
     const int64_t cover = a.r.max_pages << 4;
     std::vector<std::vector<int>> want(a.r.rows), whole(a.r.rows), parts(a.r.rows);
@@ -260,7 +261,7 @@ static void entry_points() {
   CHECK(int4_cache_extend(&pool, I, nullptr, I, I, I, (int64_t*)arena, 5, I, nullptr) == INT4DQ_OK && calls == 2, "extend");
   CHECK(int4_cache_append(&c, &r, &t, P, 512, 128, 4, P, 256, 128, P, 256, 128, 2, P, nullptr) == INT4DQ_OK && calls == 3, "append");
   auto attend = [&](int64_t sinks, const int32_t* shared, int64_t window, void* ws, int64_t bytes) {
-    return int4_cache_attention_ex(&c, &r, P, 512, 128, 1, 4, 1.0f, 1, window, sinks, shared, P, nullptr, ws, bytes, nullptr);
+    return int4_cache_attention_ex(&c, &r, P, 512, 128, 1, 4, 1.0f, 1, window, sinks, shared, -1, P, nullptr, ws, bytes, nullptr);
   };
   CHECK(attend(4, nullptr, 100, P, 256) == INT4DQ_OK && calls == 4 && shared_calls == 0, "sinks");
   CHECK(attend(0, I, 0, P, 256) == INT4DQ_OK && calls == 4 && shared_calls == 1, "shared");
@@ -269,11 +270,11 @@ static void entry_points() {
   CHECK(attend(4, nullptr, -1, P, 256) == INT4DQ_EINVAL && strstr(int4_last_error(), "int4_cache_attention_ex"), "window");
   CHECK(attend(4, I, 9, arena + 16, 256) == INT4DQ_EINVAL && strstr(int4_last_error(), "aligned"), "workspace alignment");
   CHECK(attend(4, I, 9, nullptr, 256) == INT4DQ_EINVAL, "no workspace");
-  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 4, 0) == 512, "workspace");
-  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 4, 1) == 1024, "workspace of shared tokens");
-  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 5, 1) == -1, "workspace: q_heads");
+  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 4, 0, -1) == 512, "workspace");
+  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 4, 1, -1) == 1024, "workspace of shared tokens");
+  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 5, 1, -1) == -1, "workspace: q_heads");
   r.rows = 0;
-  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 4, 1) == 0, "no rows, no workspace");
+  CHECK(int4_cache_attention_ex_workspace_bytes(&c, &r, 4, 1, -1) == 0, "no rows, no workspace");
   CHECK(attend(4, I, 9, P, 256) == INT4DQ_OK && calls == 4 && shared_calls == 2, "no rows");
 }
 

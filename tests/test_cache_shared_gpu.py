@@ -32,11 +32,12 @@ def batch(rng, heads, D, group, affine, page, shared_pages, lengths, new, spare=
     return m, table, starts
 
 
-def check(dq, m, table, lengths, starts, q, dtype, shared, window=0, sinks=0, cache=None, **kw):
+def check(dq, m, table, lengths, starts, q, dtype, shared, window=0, sinks=0, cache=None, share_from=1, **kw):
+    """share_from: 1, whatever it costs; None: where it pays."""
     cache = cache or cache_of(dq, m)
     n = torch.tensor([shared], dtype=torch.int32, device=DEV)
     return check_attention(dq, Sinks(m, sinks), table, lengths, starts, q, dtype, window=window, sinks=sinks, shared=n,
-                           cache=cache, **kw)
+                           cache=cache, share_from=share_from, **kw)
 
 
 CASES = [  # D, group, affine, heads, ratio, page, dtype, shared pages, own tokens, new rows
@@ -65,8 +66,11 @@ def test_shared(dq, D, group, affine, heads, ratio, page, dtype, pages, own, new
     for shared in (pages * page, pages * page - 37, 64 * (pages * page // 64) // 2 + 5, 3, 0, -8):
         say("case: shared", D, group, affine, heads, ratio, page, own, new, shared)
         check(dq, m, table, lengths, starts, q, dtype, shared, cache=cache)
+        check(dq, m, table, lengths, starts, q, dtype, shared, cache=cache, share_from=None)
     if set(new) == {1}:
         check(dq, m, table, lengths, None, q, dtype, pages * page, cache=cache)
+    check(dq, m, table, lengths, starts, q, dtype, pages * page, cache=cache, share_from=pages * page)
+    check(dq, m, table, lengths, starts, q, dtype, pages * page, cache=cache, share_from=pages * page + 1)
     shared = pages * page - 11
     for window, sinks in ((20, 0), (500, 0), (20, 7), (700, 90), (pages * page // 2, 30), (60, 2 ** 31)):
         say("case: shared, window", window, sinks)
@@ -119,7 +123,7 @@ def test_workspaces(dq):
     m, table, starts = batch(rng, 2, 64, 64, False, 64, 19, lengths, new)
     cache = cache_of(dq, m)
     q = rounded(rng.normal(size=(3, 4, 64)).astype(np.float32), BF16)
-    n = dq.cache_attention_workspace_bytes(cache, 3, 3, 4, shared=True)
+    n = dq.cache_attention_workspace_bytes(cache, 3, 3, 4, shared=True, share_from=1)
     assert n >= dq.cache_attention_workspace_bytes(cache, 3, 3, 4) > 0
     outs = []
     for size in (n, n + 4096, n // 2, 0):
@@ -138,18 +142,18 @@ def test_in_a_graph(dq):
     n, s = dev(lengths), torch.tensor([1152], dtype=torch.int32, device=DEV)
     q = rounded(rng.normal(size=(5, 2, 64)).astype(np.float32), F16)
     qd = dev(q).to(F16)
-    ws = dq.cache_attention_workspace(cache, 5, 5, 2, shared=True)
-    dq.int4_cache_attention(qd, cache, t, n, shared=s, workspace=ws)
+    ws = dq.cache_attention_workspace(cache, 5, 5, 2, shared=True, share_from=400)
+    dq.int4_cache_attention(qd, cache, t, n, shared=s, workspace=ws, share_from=400)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         n += 7
-        out = dq.int4_cache_attention(qd, cache, t, n, shared=s, workspace=ws)
+        out = dq.int4_cache_attention(qd, cache, t, n, shared=s, workspace=ws, share_from=400)
     for i, shared in enumerate((1152, 0, 700, 1100, 1152)):
         s.fill_(shared)
         graph.replay()
         torch.cuda.synchronize()
-        want, _ = check(dq, m, table, lengths + 7 * (i + 1), None, q, F16, shared, cache=cache, workspace=ws)
+        want, _ = check(dq, m, table, lengths + 7 * (i + 1), None, q, F16, shared, cache=cache, workspace=ws, share_from=400)
         assert torch.equal(out, want), i
 
 
