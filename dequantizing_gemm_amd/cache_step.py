@@ -22,7 +22,7 @@ import ctypes
 import torch
 
 from . import _gpu, _raise, lib
-from .cache import (ROWS_DTYPES, Int4Cache, _call, _int32, _is_cache, _plan, _raw_stream, _rows_array)
+from .cache import ROWS_DTYPES, Int4Cache, _is_cache, _raw_stream, _rows_array, _RowsStruct
 
 __all__ = ["int4_cache_release", "int4_cache_extend", "int4_cache_append"]
 
@@ -53,43 +53,57 @@ for _name, (_res, _args) in CACHE_STEP_SIGNATURES.items():
     _fn.restype, _fn.argtypes = _res, _args
 
 
-def _flat(name, t, dtype, size, device):
-    """A contiguous GPU vector of `size` elements, on `device` where that is given."""
+_Tensor, _int32_type = torch.Tensor, torch.int32
+
+# A step's calls are short (5 us on the GPU): checks are put as one expression each, and
+# what fails it goes through the checks that say what is wrong.
+
+
+def _vector(t, name, dtype, size, index):
+    """Address of a contiguous vector of `size` elements on the GPU `index`."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == 1 and t.shape[0] == size \
+            and t.is_contiguous():
+        return t.data_ptr()
     _gpu(t, name, dtype, 1)
-    if size is not None and t.shape[0] != size:
+    if t.shape[0] != size:
         raise ValueError(f"{name} must have {size} entries (got {t.shape[0]})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+
+
+def _table(t, index):
+    """Address, row stride, rows and columns of a page table."""
+    if not isinstance(t, _Tensor) or t.dtype is not _int32_type or t.dim() != 2:
+        raise ValueError("page_table must be an int32 tensor of 2 dimension(s)")
+    if t.get_device() != index:
+        raise ValueError(f"page_table must be on cuda:{index} (got {t.device})")
+    batch, max_pages = t.shape
+    row, column = t.stride()
+    if batch <= 1 or max_pages == 0:
+        row = max_pages
+    if column != 1 and max_pages > 1 and batch > 0:
+        raise ValueError("page_table must be contiguous in its last dimension")
+    if row < max_pages:
+        raise ValueError("page_table rows must not overlap")
+    return t.data_ptr(), row, batch, max_pages
 
 
 def _pool(page_table, lengths, free, count, page_size):
-    """The pool descriptor, checked."""
-    _flat("free", free, torch.int32, None, None)
-    dev = free.device
-    if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32 or page_table.dim() != 2:
-        raise ValueError("page_table must be an int32 tensor of 2 dimension(s)")
-    if page_table.device != dev:
-        raise ValueError(f"page_table must be on {dev} (got {page_table.device})")
-    batch, max_pages = page_table.shape
-    if page_table.numel() and max_pages > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table must be contiguous in its last dimension")
-    stride = page_table.stride(0) if batch > 1 else max_pages
-    if stride < max_pages:
-        raise ValueError("page_table rows must not overlap")
-    _flat("lengths", lengths, torch.int32, batch, dev)
-    _flat("count", count, torch.int32, 2, dev)
-    return _PoolStruct(page_table.data_ptr(), stride, max_pages, batch, page_size, free.data_ptr(), free.shape[0])
+    """The pool descriptor, checked, with the GPU, the batch and the addresses of lengths and count."""
+    _gpu(free, "free", _int32_type, 1)
+    index = free.get_device()
+    at, stride, batch, max_pages = _table(page_table, index)
+    n, c = _vector(lengths, "lengths", _int32_type, batch, index), _vector(count, "count", _int32_type, 2, index)
+    return _PoolStruct(at, stride, max_pages, batch, page_size, free.data_ptr(), free.shape[0]), index, batch, n, c
 
 
-def _pool_call(fn, what, device, pool, *args):
-    """Calls a C entry point with `device` current, on its current stream."""
-    index = device.index
+def _on(index, fn, what, *args):
+    """Calls a C entry point with the GPU `index` current, on its current stream; a
+    status other than OK is raised."""
     if torch.cuda.current_device() == index:
-        rc = fn(ctypes.addressof(pool), *args, _raw_stream(index))
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = fn(ctypes.addressof(pool), *args, _raw_stream(index))
+            rc = fn(*args, _raw_stream(index))
     if rc:
         _raise(rc, what)
 
@@ -102,17 +116,17 @@ def int4_cache_release(page_table: torch.Tensor, lengths: torch.Tensor, free: to
     0 for those sequences, and the free pages. ``shared`` int32 [1]: the pages
     wholly in the first shared[0] tokens belong to other sequences too and are kept.
     ``out``: the two tensors to fill, which may be ``lengths`` and ``count``."""
-    pool = _pool(page_table, lengths, free, count, page_size)
-    dev, batch = free.device, page_table.shape[0]
-    if not isinstance(done, torch.Tensor) or done.dtype not in (torch.bool, torch.uint8):
+    pool, index, batch, n, c = _pool(page_table, lengths, free, count, page_size)
+    if not isinstance(done, _Tensor) or done.dtype not in (torch.bool, torch.uint8):
         raise ValueError("done must be a bool or uint8 tensor")
-    ended = _flat("done", done, done.dtype, batch, dev)
-    common = None if shared is None else _flat("shared", shared, torch.int32, 1, dev)
+    ended = _vector(done, "done", done.dtype, batch, index)
+    common = None if shared is None else _vector(shared, "shared", _int32_type, 1, index)
     if out is None:
-        out = (torch.empty(batch, dtype=torch.int32, device=dev), torch.empty(2, dtype=torch.int32, device=dev))
-    to = [_flat(n, t, torch.int32, s, dev) for n, t, s in zip(("out[0]", "out[1]"), out, (batch, 2))]
-    _pool_call(lib.int4_cache_release, "int4_cache_release", dev, pool, lengths.data_ptr(), ended, count.data_ptr(), common,
-               *to)
+        out = (lengths.new_empty(batch), count.new_empty(2))
+        to = (out[0].data_ptr(), out[1].data_ptr())
+    else:
+        to = (_vector(out[0], "out[0]", _int32_type, batch, index), _vector(out[1], "out[1]", _int32_type, 2, index))
+    _on(index, lib.int4_cache_release, "int4_cache_release", ctypes.addressof(pool), n, ended, c, common, *to)
     return out
 
 
@@ -127,22 +141,33 @@ def int4_cache_extend(page_table: torch.Tensor, lengths: torch.Tensor, free: tor
     -1 where it has none (None with ``slots=False``); and the free pages with how many
     more were needed. ``out``: the four to fill, of which the first and last may be
     ``lengths`` and ``count``."""
-    pool = _pool(page_table, lengths, free, count, page_size)
-    dev, batch = free.device, page_table.shape[0]
-    added = None if new is None else _flat("new", new, torch.int32, batch, dev)
+    pool, index, batch, n, c = _pool(page_table, lengths, free, count, page_size)
+    added = None if new is None else _vector(new, "new", _int32_type, batch, index)
     if rows is None:
         if slots and new is not None and out is None:
             raise ValueError("rows must be given with new")
         rows = batch if new is None else out[2].shape[0] if out is not None and out[2] is not None else 0
     if out is None:
-        def make(n, dtype=torch.int32):
-            return torch.empty(n, dtype=dtype, device=dev)
-        out = (make(batch), make(batch + 1), make(rows, torch.int64) if slots else None, make(2))
-    at = None if out[2] is None else _flat("out[2]", out[2], torch.int64, rows, dev)
-    to = [_flat(f"out[{i}]", out[i], torch.int32, s, dev) for i, s in ((0, batch), (1, batch + 1), (3, 2))]
-    _pool_call(lib.int4_cache_extend, "int4_cache_extend", dev, pool, lengths.data_ptr(), added, count.data_ptr(), to[0],
-               to[1], at, rows, to[2])
+        out = (lengths.new_empty(batch), lengths.new_empty(batch + 1),
+               lengths.new_empty(rows, dtype=torch.int64) if slots else None, count.new_empty(2))
+        to = [None if t is None else t.data_ptr() for t in out]
+    else:
+        to = [None if t is None and i == 2 else _vector(t, f"out[{i}]", d, s, index)
+              for i, (t, d, s) in enumerate(zip(out, (_int32_type, _int32_type, torch.int64, _int32_type),
+                                                (batch, batch + 1, rows, 2)))]
+    _on(index, lib.int4_cache_extend, "int4_cache_extend", ctypes.addressof(pool), n, added, c, to[0], to[1], to[2], rows,
+        to[3])
     return out
+
+
+def _rows_of(cache, index, t, name, heads):
+    """Rows, row and head stride of a [rows, heads, head_dim] tensor with channels side by side."""
+    if isinstance(t, _Tensor) and t.get_device() == index and t.dim() == 3:
+        rows, h, d = t.shape
+        row, head, channel = t.stride()
+        if h == heads and d == cache.head_dim and (channel == 1 or d == 1):
+            return rows, row, head
+    raise ValueError(_rows_array(cache, t, name, heads))         # (which says what is wrong)
 
 
 def int4_cache_append(cache: Int4Cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
@@ -161,33 +186,43 @@ def int4_cache_append(cache: Int4Cache, q: torch.Tensor, k: torch.Tensor, v: tor
     whose position is below 0 or past ``rope`` gives 0 and writes nothing. ``out``: a
     contiguous tensor to fill, which may be ``q``."""
     _is_cache(cache)
-    q_heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
-    qs = _rows_array(cache, q, "q", q_heads)
-    ks, vs = _rows_array(cache, k, "k", cache.heads), _rows_array(cache, v, "v", cache.heads)
-    if q.dtype not in ROWS_DTYPES or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError(f"q, k and v must be float32, float16 or bfloat16, all the same (got {q.dtype}, {k.dtype}, {v.dtype})")
-    rows = q.shape[0]
-    if k.shape[0] != rows or v.shape[0] != rows:
-        raise ValueError(f"q has {rows} rows, k {k.shape[0]}, v {v.shape[0]}")
-    plan = _plan(cache, page_table, lengths, starts, rows)
-    weights = [None if w is None else _flat(n, w, torch.float32, cache.head_dim, cache.device)
-               for n, w in (("q_norm", q_norm), ("k_norm", k_norm))]
-    turn = (None, 0, 0, 0)
-    if rope is not None:
-        if not isinstance(rope, torch.Tensor) or rope.dtype != torch.float32 or rope.dim() != 2:
-            raise ValueError("rope must be a float32 tensor of 2 dimensions")
-        if rope.device != cache.device:
-            raise ValueError(f"rope must be on {cache.device} (got {rope.device})")
-        if rope.shape[1] > 1 and rope.stride(1) != 1:
-            raise ValueError("rope must be contiguous in its last dimension")
-        turn = (rope.data_ptr(), rope.stride(0) if rope.shape[0] > 1 else rope.shape[1], rope.shape[0], rope.shape[1])
-    transform = _TransformStruct(*weights, eps, *turn, bool(interleaved))
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    index = cache.device.index
+    q_heads = q.shape[1] if isinstance(q, _Tensor) and q.dim() == 3 else -1
+    rows, *qs = _rows_of(cache, index, q, "q", q_heads)
+    k_rows, *ks = _rows_of(cache, index, k, "k", cache.heads)
+    v_rows, *vs = _rows_of(cache, index, v, "v", cache.heads)
+    dtype = q.dtype
+    if dtype not in ROWS_DTYPES or k.dtype is not dtype or v.dtype is not dtype:
+        raise ValueError(f"q, k and v must be float32, float16 or bfloat16, all the same (got {dtype}, {k.dtype}, {v.dtype})")
+    if k_rows != rows or v_rows != rows:
+        raise ValueError(f"q has {rows} rows, k {k_rows}, v {v_rows}")
+    at, stride, batch, max_pages = _table(page_table, index)
+    n = _vector(lengths, "lengths", _int32_type, batch, index)
+    s = None if starts is None else _vector(starts, "starts", _int32_type, batch + 1, index)
+    if s is None and rows != batch:
+        raise ValueError(f"without starts there is one row a sequence (got {rows} rows, {batch} sequences)")
+    plan = _RowsStruct(at, stride, max_pages, n, s, batch, rows)
+    qw = None if q_norm is None else _vector(q_norm, "q_norm", torch.float32, cache.head_dim, index)
+    kw = None if k_norm is None else _vector(k_norm, "k_norm", torch.float32, cache.head_dim, index)
+    if rope is None:
+        transform = _TransformStruct(qw, kw, eps, None, 0, 0, 0, bool(interleaved))
     else:
-        _gpu(out, "out", q.dtype, 3)
-        if tuple(out.shape) != tuple(q.shape) or out.device != q.device:
+        if not isinstance(rope, _Tensor) or rope.dtype is not torch.float32 or rope.dim() != 2:
+            raise ValueError("rope must be a float32 tensor of 2 dimensions")
+        if rope.get_device() != index:
+            raise ValueError(f"rope must be on {cache.device} (got {rope.device})")
+        positions, rotary = rope.shape
+        row, channel = rope.stride()
+        if channel != 1 and rotary > 1:
+            raise ValueError("rope must be contiguous in its last dimension")
+        transform = _TransformStruct(qw, kw, eps, rope.data_ptr(), row if positions > 1 else rotary, positions, rotary,
+                                     bool(interleaved))
+    if out is None:
+        out = q.new_empty(q.shape)
+    else:
+        _gpu(out, "out", dtype, 3)
+        if out.shape != q.shape or out.get_device() != index:
             raise ValueError(f"out must be {tuple(q.shape)} on {q.device}")
-    _call(cache, lib.int4_cache_append, "int4_cache_append", ctypes.addressof(plan), ctypes.addressof(transform),
-          q.data_ptr(), *qs, q_heads, k.data_ptr(), *ks, v.data_ptr(), *vs, ROWS_DTYPES[q.dtype], out.data_ptr())
+    _on(index, lib.int4_cache_append, "int4_cache_append", cache._ref, ctypes.addressof(plan), ctypes.addressof(transform),
+        q.data_ptr(), *qs, q_heads, k.data_ptr(), *ks, v.data_ptr(), *vs, ROWS_DTYPES[dtype], out.data_ptr())
     return out
