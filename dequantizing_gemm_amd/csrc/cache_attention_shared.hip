@@ -147,7 +147,8 @@ hipError_t launch_width(const AttentionArgs& whole, const Parts& p, const Worksp
   }
   // one launch where tiles are as high, so that the sequences' own tokens fill in; not with
   // the form for prompts, which fills the GPU (917 us together, 850 apart)
-  const bool together = p.own.tile_rows == p.shared.tile_rows && p.own.tile_rows != kWideRows;
+  const bool together = p.own.tile_rows == p.shared.tile_rows && p.own.tile_rows != kWideRows &&
+                        ((int64_t)p.own.units + p.shared.units) * a.c.heads < (1 << 24);          // 2^32 threads
   const Second<true> second{together ? (unsigned)(p.own.units * a.c.heads) : 0, p.shared, ws2};
   hipError_t e = launch_attention_width<C, true>(a, p.own, ws, second, stream);
   if (e != hipSuccess) return e;
