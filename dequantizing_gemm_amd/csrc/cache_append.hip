@@ -419,8 +419,12 @@ __global__ __launch_bounds__(256) void cache_append_steps_kernel(AppendArgs a, A
 template <int DT, int L, bool WIDE>
 hipError_t launch_lanes(const AppendArgs& a, AppendPlan p, int dtype, hipStream_t stream) {
   constexpr int ROWS = 256 / L;
-  if (!a.r.starts || a.r.rows < 8 * (int64_t)a.r.batch) {
-    const int64_t items = a.r.rows * (a.q_heads + 2 * a.c.heads);
+  // Row by row while that takes one short launch or a block of 64 positions would hold
+  // few rows. Measured, row by row against by positions, 8 + 32 heads of 128: 8 sequences
+  // of 32 rows 7 and 12 us, of 256 23 and 25, of 512 39 and 34, of 2000 185 and 108; 64
+  // of 48 33 and 41, of 64 42 and 40; 512 of 16 86 and 96, of 24 148 and 123.
+  const int64_t items = a.r.rows * (a.q_heads + 2 * a.c.heads);
+  if (!a.r.starts || a.r.rows < 20 * (int64_t)a.r.batch || items * a.c.D <= 20000000) {
     hipLaunchKernelGGL((cache_append_rows_kernel<DT, L, WIDE>), dim3((unsigned)((items + ROWS - 1) / ROWS)), dim3(256), 0,
                        stream, a, p);
     return hipGetLastError();

@@ -183,33 +183,62 @@ def test_no_rows(dq):
     assert_same_bytes(cache, m)
 
 
-def test_many_rows(dq):
-    """Enough rows that a block takes several heads: the same bits as few rows at a time."""
-    rng = np.random.default_rng(8)
-    H, R, D, S = 8, 4, 128, 64
-    lengths = [9000, 9100, 1500]
-    table, pages, starts = plan(rng, lengths, lengths, S)
-    T = int(starts[-1])
+MANY = [  # D, group, affine, heads, query heads, page, dtype, rotary, interleaved, norm, lengths, new rows, elements before the rows
+    (128, 64, True, 8, 32, 64, BF16, 128, False, True, [2000, 1800, 150], [2000, 1700, 21], 0),
+    (128, 128, False, 4, 60, 16, F16, 64, False, True, [2600, 90], [2581, 70], 0),
+    (64, 32, True, 12, 12, 16, F32, 64, False, True, [5000, 5003], [4900, 4801], 0),
+    (64, 64, False, 20, 60, 32, BF16, 64, True, False, [4100], [4090], 0),
+    (80, 32, True, 10, 30, 16, F16, 80, False, True, [4000, 1800], [4000, 1790], 0),
+    (96, 96, False, 10, 40, 16, BF16, 48, False, True, [3000, 900], [2990, 900], 0),
+    (96, 64, True, 10, 40, 64, F32, 96, True, True, [3700, 77], [3650, 41], 0),
+    (72, 128, False, 10, 40, 16, BF16, 72, False, True, [4000, 900], [3900, 900], 0),
+    (192, 64, True, 8, 24, 16, BF16, 192, False, True, [2200, 700], [2190, 700], 0),
+    (192, 128, False, 8, 24, 16, F16, 0, False, True, [2200, 700], [2190, 700], 0),
+    (256, 128, False, 4, 24, 32, BF16, 256, False, True, [2000, 600], [1999, 599], 0),
+    (256, 32, True, 4, 24, 16, F32, 128, True, True, [2000, 600], [1999, 599], 0),
+    (250, 64, False, 4, 24, 16, F16, 250, False, True, [2000, 600], [1999, 599], 0),
+    (128, 128, True, 8, 32, 64, BF16, 128, False, True, [2000, 1800, 150], [2000, 1700, 21], 3),
+    (33, 32, False, 16, 64, 16, F16, 32, False, True, [6600], [6550], 0),
+    (2, 2, True, 60, 120, 16, BF16, 2, True, True, [45000], [44900], 0),
+]
+
+
+@pytest.mark.parametrize("D,group,affine,H,HQ,S,dtype,rotary,interleaved,norm,lengths,new,off", MANY)
+def test_many_rows(dq, D, group, affine, H, HQ, S, dtype, rotary, interleaved, norm, lengths, new, off):
+    """So many rows that they are taken by positions: the same bits as few rows at a time,
+    which go row by row; rows that no sequence owns before and behind, pages that are none,
+    positions past the rope."""
+    rng = np.random.default_rng(D + group)
+    table, pages, starts = plan(rng, lengths, new, S)
+    starts = starts + 2
+    table[0, 1], table[-1, 0] = -1, pages + 5
+    T = int(starts[-1]) + 3
+    assert T * (HQ + 2 * H) * D > 20000000 and T >= 20 * len(new)
     g = torch.Generator(device=DEV).manual_seed(1)
-    q, k, v = (torch.randn(T, h, D, generator=g, device=DEV).to(BF16) for h in (H * R, H, H))
-    rope, w = dev(rope_table(9100, 128)), dev(weights(rng, D))
-    caches = [dq.Int4Cache.empty(pages, S, H, D, 64, True) for _ in range(2)]
+    fused = torch.randn(T, (HQ + 2 * H) * D + off, generator=g, device=DEV).to(dtype)[:, off:].unflatten(1, (-1, D))
+    q, k, v = fused.split([HQ, H, H], 1)
+    rope = dev(rope_table(max(lengths) - 37, rotary)) if rotary else None
+    q_norm, k_norm = (dev(weights(rng, D)) for _ in range(2)) if norm else (None, None)
+    caches = [dq.Int4Cache.empty(pages, S, H, D, group, affine) for _ in range(2)]
+    names = [n for n in ("k_packed", "v_packed", "k_scales", "v_scales", "k_zeros", "v_zeros") if getattr(caches[0], n) is not None]
     for c in caches:
-        for t in (c.k_packed, c.v_packed, c.k_zeros, c.v_zeros, c.k_scales, c.v_scales):
-            t.zero_()
-    say("case: many rows", T)
-    kw = dict(q_norm=w, k_norm=w, rope=rope)
-    whole = dq.int4_cache_append(caches[0], q, k, v, dev(table), dev(np.array(lengths, np.int32)), dev(starts), **kw)
-    parts = []
+        for n in names:
+            getattr(c, n).zero_()
+    say("case: many rows", D, group, affine, H, HQ, dtype, rotary, interleaved, T)
+    kw = dict(q_norm=q_norm, k_norm=k_norm, rope=rope, interleaved=interleaved)
+    out = torch.full((T, HQ, D), 7.0, dtype=dtype, device=DEV)
+    whole = dq.int4_cache_append(caches[0], q, k, v, dev(table), dev(np.array(lengths, np.int32)), dev(starts), out=out, **kw)
+    assert (whole[:2] == 7).all() and (whole[-3:] == 7).all()
+    step = max(1, 19000000 // ((HQ + 2 * H) * D))
     for b, n in enumerate(lengths):
-        for at in range(0, n, 700):
-            m = min(700, n - at)
+        for at in range(0, new[b], step):
+            m = min(step, new[b] - at)
             rows = slice(int(starts[b]) + at, int(starts[b]) + at + m)
-            parts.append(dq.int4_cache_append(caches[1], q[rows], k[rows], v[rows], dev(table[b:b + 1]),
-                                              dev(np.array([at + m], np.int32)), dev(np.array([0, m], np.int32)), **kw))
-    assert torch.equal(whole, torch.cat(parts))
-    for name in ("k_packed", "v_packed", "k_scales", "v_scales", "k_zeros", "v_zeros"):
-        assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), name
+            part = dq.int4_cache_append(caches[1], q[rows], k[rows], v[rows], dev(table[b:b + 1]),
+                                        dev(np.array([n - new[b] + at + m], np.int32)), dev(np.array([0, m], np.int32)), **kw)
+            assert torch.equal(whole[rows], part)
+    for n in names:
+        assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)), n
 
 
 def test_append_in_a_graph_and_on_two_streams(dq):
