@@ -716,16 +716,16 @@ struct Span {
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // The kernels come in two forms: MORE also takes first tokens that stay visible and the
-// parts of a batch that shares tokens. What other calls run has none of that in it: as
-// one form the registers of both would not do (up to 10 more, and spills where tiles
-// fill them).
+// parts of a batch that shares tokens. What other calls run has none of that in it, which
+// takes 2 to 12 registers more and half a microsecond.
 //
-// A second share of blocks in a launch, of the shared part: those from `from` on.
+// A second share of blocks in a launch, those of the shared part: the first `blocks`,
+// since they are the longer ones.
 template <bool MORE>
 struct Second {};
 template <>
 struct Second<true> {
-  unsigned from;                         // 0: there is none
+  unsigned blocks;                       // 0: there is none
   Schedule sched;
   Workspace ws;
 };
@@ -734,16 +734,16 @@ struct Second<true> {
 template <bool MORE>
 __device__ __forceinline__ int block_of(AttentionArgs* a, Schedule* s, Workspace* ws, const Second<MORE>& second) {
   if constexpr (MORE) {
-    if (second.from == 0 || blockIdx.x < second.from) {
+    if (blockIdx.x >= second.blocks) {
       s->partial = leaves_parts(*a, *s);
-      return blockIdx.x;
+      return blockIdx.x - second.blocks;
     }
     a->part = kSharedPart;
     a->all = a->r.batch;
     a->r.batch = 1;
     *s = second.sched;
     *ws = second.ws;
-    return blockIdx.x - second.from;
+    return blockIdx.x;
   } else {
     a->sinks = 0;
     a->part = kWhole;

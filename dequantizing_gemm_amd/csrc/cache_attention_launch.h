@@ -11,7 +11,7 @@ void launch_attention_form(const AttentionArgs& a, const Schedule& s, const Work
                            const Second<MORE>& second, hipStream_t stream) {
   int64_t units = s.units;
   if constexpr (MORE)
-    if (second.from > 0) units += second.sched.units;
+    if (second.blocks > 0) units += second.sched.units;
   const dim3 grid((unsigned)(units * a.c.heads));
   if (s.tile_rows == kWideRows) {                    // plan_of asks for the forms that there are
     constexpr int QT = wide_tiles(C, C / GC, AFF);

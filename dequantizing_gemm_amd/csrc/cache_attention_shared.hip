@@ -5,11 +5,21 @@
 // both parts' sums, each taken with its own reference m: with partial sums o_i and
 // l_i over chunks i of either part, out = sum_i exp2(m_i - M) o_i / sum_i exp2(m_i - M) l_i.
 //
-// Work. The shared tokens are one sequence whose rows are those of the whole
-// batch, side by side: a tile of 128 of them reads and takes apart the shared codes
-// once, where the sequences by themselves would do so for a tile each, filled to
-// rows * ratio of 16. Each sequence's own tokens are a second call of the same
-// kernel. Both leave partial results, and one join adds them row by row.
+// Work. The shared tokens are one sequence whose rows are those of the whole batch,
+// side by side: a tile of 16, 32 or 128 of them reads and takes apart the shared codes
+// once, where the sequences by themselves would do so for a tile of 16 each, of which
+// one token fills only as many rows as there are query heads to a key head. Each
+// sequence's own tokens are cut as in a call of its own. Both leave partial results, and
+// one join adds them row by row: bound by the latency of a chain of four loads (64
+// sequences, 32 query heads of 128, 15 chunks a row: 6.8 us).
+//
+// What bounds it (8 x 4 heads of 128, groups of 64, bfloat16, 64 sequences of 10 to 1500
+// own tokens on 32768 shared ones, 95 us in all). The shared part in tiles of 32 rows 73 us,
+// 470 TFLOP/s: the VALU, busy for 65% of it, which takes codes apart for four tiles of a
+// head and block; in tiles of 128 it is 60 us and a longer join. The own part 23 us:
+// latency, at most 24 steps of 64 tokens on four wavefronts. Both in one kernel, with
+// tiles of 32 and 16 rows, was 92 us here, but 67 against 46 for 200 sequences of few own
+// tokens, whose blocks then have the registers of the taller tiles.
 #include "cache_attention_kernel.h"
 #include "cache_step.h"
 
@@ -41,14 +51,17 @@ int64_t sharing_pays(const RowsView& r, int ratio) {
   return r.batch >= 8 && rows > 64 * (int64_t)r.batch && rows <= 640 * (int64_t)r.batch && rows <= 16384 ? 16384 : 0;
 }
 
-// The tiles of the shared part. Measured with the sequences' own in tiles of 16 rows,
-// tiles of 16 (in one launch), 32 and 128 rows: 64 rows 24, 29 and 40 us with 8192 shared
-// tokens, 45, 47 and 59 with 32768; 256 rows 44, 43 and 49, 104, 92 and 92; 512 rows 71, 67
-// and 71, 198, 169 and 162; 1024 rows 78, 72 and 77 with 1984.
-int shared_tile_rows(const CacheView& c, int64_t rows) {
+// The tiles of the shared part, for the number of its rows and of the tokens that the
+// page table covers, which the shared ones may be. Measured, 300 own tokens, in tiles of 16
+// (one launch with the sequences' own), 32 and 128 rows: 128 rows 24, 30 and 42 us with
+// 4032 shared tokens, 55, 55 and 61 with 32768; 256 rows 29, 33 and 45 with 1984, 44, 45 and
+// 51 with 8192, 87, 81 and 82 with 32768; 512 rows 47, 52 and 61, 68, 69 and 73, 154, 141
+// and 132; 1024 rows 70, 75 and 78, 109, 108 and 106, 300, 249 and 224.
+constexpr int64_t kLongTable = 16384;
+int shared_tile_rows(const CacheView& c, int64_t rows, int64_t cover) {
   const int groups = c.C / scale_blocks(c), most = 16 * max_tiles(c.C, groups, c.affine);
-  if (rows > 1024 && wide_tiles(c.C, groups, c.affine) > 0) return kWideRows;
-  return rows > 128 ? most : 16;
+  if (rows >= (cover < kLongTable ? 2048 : 1024) && wide_tiles(c.C, groups, c.affine) > 0) return kWideRows;
+  return rows >= 256 && cover >= kLongTable ? most : 16;
 }
 
 // False: sharing would not pay, or cannot be. from < 0: where it pays.
@@ -62,7 +75,7 @@ bool plan_parts(const CacheView& c, const RowsView& r, int ratio, int64_t from, 
   // A join follows in any case: blocks of 8 steps, not 16 (24 sequences' rows, 1984
   // shared tokens: 21.1 -> 17.3 us; of 4: 16.2, but 33.1 -> 37.5 with 32768).
   p->own = plan_for(c, r, ratio, tile_rows_of(c, r, ratio), 8);
-  p->shared = plan_for(c, one, ratio, shared_tile_rows(c, r.rows * ratio), 8);
+  p->shared = plan_for(c, one, ratio, shared_tile_rows(c, r.rows * ratio, r.max_pages << c.page_shift), 8);
   if (p->own.target == 0 || p->shared.target == 0) return false;
   p->own.partial = p->shared.partial = 1;
   p->own_bytes = (workspace_bytes(p->own, c.heads, c.C, r.batch) + 255) / 256 * 256;
@@ -149,7 +162,7 @@ hipError_t launch_width(const AttentionArgs& whole, const Parts& p, const Worksp
   // the form for prompts, which fills the GPU (917 us together, 850 apart)
   const bool together = p.own.tile_rows == p.shared.tile_rows && p.own.tile_rows != kWideRows &&
                         ((int64_t)p.own.units + p.shared.units) * a.c.heads < (1 << 24);          // 2^32 threads
-  const Second<true> second{together ? (unsigned)(p.own.units * a.c.heads) : 0, p.shared, ws2};
+  const Second<true> second{together ? (unsigned)(p.shared.units * a.c.heads) : 0, p.shared, ws2};
   hipError_t e = launch_attention_width<C, true>(a, p.own, ws, second, stream);
   if (e != hipSuccess) return e;
   if (!together) {
@@ -179,7 +192,13 @@ extern template hipError_t launch_attention_width<8, true>(const AttentionArgs&,
 
 int64_t cache_attention_shared_workspace(const CacheView& c, const RowsView& r, int ratio, int64_t from) {
   Parts p;
-  return plan_parts(c, r, ratio, from, &p) ? p.own_bytes + p.shared_bytes : 0;
+  int64_t most = plan_parts(c, r, ratio, from, &p) ? p.own_bytes + p.shared_bytes : 0;
+  if ((r.max_pages << c.page_shift) >= kLongTable) { // a call whose table is shorter may cut finer
+    RowsView shorter = r;
+    shorter.max_pages = (kLongTable - 1) >> c.page_shift;
+    if (plan_parts(c, shorter, ratio, from, &p) && p.own_bytes + p.shared_bytes > most) most = p.own_bytes + p.shared_bytes;
+  }
+  return most;
 }
 
 hipError_t launch_cache_attention_shared(const AttentionArgs& args, int64_t from, void* workspace, int64_t bytes,
