@@ -53,7 +53,10 @@
 // MB in 67 us. One sequence of 131071 tokens, groups of 32 with zero points: the
 // VALU, which takes codes apart and applies scales; 159 MB in 50 us. A prompt of
 // 4096 tokens: 137 GFLOP in 192 us, the VALU busy for 56% of it and the matrix pipes
-// for 28%, with little overlap at two wavefronts a SIMD.
+// for 28%, with little overlap at two wavefronts a SIMD. With a window and first tokens,
+// 32 sequences of 500 to 16001 tokens, window 2048: 64 MB in 22 us, latency of 12 steps a
+// block; prompts in chunks, 4 of 553 to 1024 tokens, 4 x 6 heads of 96, window 1500: 47
+// GFLOP in 130 us, 149 tiles on 128 places.
 #pragma once
 
 #include <type_traits>

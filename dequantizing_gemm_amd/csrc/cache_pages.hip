@@ -5,6 +5,12 @@
 // Mathematics: exclusive sums over the batch of new tokens (starts) and of the
 // pages they need; the i-th page of sequence b is the free page
 // count - 1 - (pages needed before b) - i, whatever else runs.
+//
+// Work. One block of 1024 threads, a thread a sequence for the sums and then a thread a
+// page: the sums need each other, and a step's work is small. Bound by latency: 128
+// sequences of one new token 5.2 us, 9 ended ones' 282 pages given back 3.9 us, 72447 new
+// tokens of 46 sequences, 4534 pages, 7.7 us and their slots, on the whole GPU, 3.6 us;
+// 8000 sequences of one new token 25 us.
 #include "cache_step.h"
 #include "lanes.h"
 
@@ -183,8 +189,9 @@ __global__ __launch_bounds__(256) void cache_slots_kernel(PagesArgs a, const int
   slots[t] = slot;
 }
 
-// From more rows than this, their slots are written by a kernel of their own, on
-// the whole GPU, instead of by the one block that takes the pages.
+// From more rows than this, their slots are written by a kernel of their own, on the
+// whole GPU, instead of by the one block that takes the pages, which takes a microsecond
+// for 1024 of them (16 sequences: 1008 rows 6.8 us, 2016 7.8, 2064 8.1, 64512 10.8).
 constexpr int64_t kRowsOfOneBlock = 2048;
 
 }  // namespace

@@ -107,6 +107,8 @@ typedef struct int4_cache_transform {
  *           0 and its key and value are not written.
  *   cache   out: as int4_cache_write of the transformed keys (as binary32, they are
  *           not rounded to `dtype` between) and of the values.
+ * Preconditions not checked: q, k and v, weights, cosines and sines are finite, and
+ * with eps = 0 no row that is normalised is all zeros.
  * Errors: those of int4_cache_write, and EINVAL for q_heads outside 1 .. 65535,
  * rows * (heads + q_heads) above 2^25 or batch * heads above 2^20, a rotary_dim that
  * is odd or outside 2 .. head_dim (where there is a rope), rope_positions outside

@@ -168,8 +168,38 @@ static void attention() {
         x.all = B;
         x.r.batch = r.batch = 1;
       }
-      Schedule s = plan_of(x.c, r, x.ratio);
+      const int groups = x.c.C / scale_blocks(x.c), tall = 16 * max_tiles(x.c.C, groups, x.c.affine);
+      const int heights[] = {tile_rows_of(x.c, r, x.ratio), 16, tall, wide_tiles(x.c.C, groups, x.c.affine) > 0 ? kWideRows : 16};
+      Schedule s = plan_for(x.c, r, x.ratio, heights[pick(0, 3)], pick(0, 1) ? 8 : 16);
       s.partial = x.part != kWhole;
+      // the cut: blocks inside the grid, partial results inside the workspace
+      if (s.target > 0) {
+        double work = 0, tiles = 0;
+        int longest = 0;
+        for (int b = 0; b < x.r.batch; ++b) {
+          const SequenceWork w = sequence_work(x, s.tile_rows, b);
+          work += (double)w.tiles * w.steps;
+          tiles += w.tiles;
+          if (w.tiles > 0) longest = std::max(longest, w.steps);
+        }
+        const int per = steps_per_block(s, (float)work, (float)tiles, longest, [&](int n) {
+          int sum = 0;
+          for (int b = 0; b < x.r.batch; ++b) {
+            const SequenceWork w = sequence_work(x, s.tile_rows, b);
+            if (w.tiles > 0) sum += (chunks_of(w.steps, n) - 1) * w.tiles;
+          }
+          return sum;
+        });
+        int64_t all = 0, slots = 0;
+        for (int b = 0; b < x.r.batch; ++b) {
+          const SequenceWork w = sequence_work(x, s.tile_rows, b);
+          const int chunks = chunks_of(w.steps, per);
+          all += (int64_t)w.tiles * chunks;
+          if (chunks > 1 || leaves_parts(x, s)) slots += (int64_t)w.tiles * chunks;
+        }
+        CHECK(all <= s.units, "blocks inside the grid");
+        CHECK(slots <= workspace_slots(s), "partial results inside the workspace");
+      }
       if (s.target == 0) s.target = 1;
       int64_t blocks = 0;
       const int head = (int)pick(0, x.ratio - 1);
