@@ -186,7 +186,9 @@ hipError_t launch_width(const AttentionArgs& a, const Schedule& s, const Workspa
   if (e == hipSuccess)
     e = sink_end(a) > 0 ? launch_attention_width<C, true>(a, s, ws, {}, stream) : launch_attention_width<C, false>(a, s, ws, {}, stream);
   if (e != hipSuccess || s.target == 0) return e;
-  const unsigned rows = (unsigned)(a.r.starts || a.ratio > 4 ? 4 : a.ratio);
+  // few tiles of many rows after a last round: more blocks for each (18 tiles in 7 chunks, 4
+  // blocks 172 us with the attention, 16 blocks 166)
+  const unsigned rows = s.last_round ? 16 : (unsigned)(a.r.starts || a.ratio > 4 ? 4 : a.ratio);
   hipLaunchKernelGGL(cache_attention_join_kernel<C>, dim3((unsigned)(workspace_slots(s) * a.c.heads), rows), dim3(256),
                      0, stream, a, s, ws);
   return hipGetLastError();
@@ -229,12 +231,23 @@ hipError_t launch_cache_attention(const AttentionArgs& a, void* workspace, int64
   // of 3 to 5 rows 20.2 -> 22.8.
   const bool few = a.r.batch <= 4 && a.r.rows * a.ratio <= 4 * tile_rows;
   Schedule s = plan_for(a.c, a.r, a.ratio, tile_rows, sink_end(a) > 0 && (few || tile_rows == kWideRows) ? 8 : 16);
-  // Prompts' tiles with a short window are as long as each other, and a join costs more
-  // than the last round's empty places: not cut. 149 tiles on 128 places, window 1500,
-  // 147.5 -> 129 us, 300 82 -> 54, 3000 206 -> 209; 77 tiles 80 -> 78, 48 tiles 58 either way.
-  if (sink_end(a) > 0 && tile_rows == kWideRows && a.window < 2560 && 3 * (a.r.rows * a.ratio / tile_rows) >= s.target) {
-    s.units -= s.target * (s.crowded ? 2 : 1);
-    s.target = s.crowded = s.planned = 0;
+  if (sink_end(a) > 0 && tile_rows == kWideRows) {
+    // Prompts' tiles with a window are about as long as each other: with more tiles than
+    // places only those of the last round are cut, over all places. 149 tiles on 128
+    // places, against as many cuts as without first tokens and none at all: window 1500,
+    // 148, 129 and 108 us, 3000 205, 207 and 170, 6000 321, 332 and 278; 274 tiles 194, 194
+    // and 166. Where fewer tiles are cut for a short window, the join costs more than the
+    // empty places, and so it does for the last round where a tile has less than two
+    // blocks' steps: 77 tiles, window 1500, 80 us and uncut 77, 122 tiles 83 and 79; 149
+    // tiles, window 300, 83 and 55.
+    const int64_t tiles = a.r.rows * a.ratio / tile_rows, run = a.window / kStep + (sink_end(a) - 1) / kStep + 2;
+    const bool last_round = tiles >= s.target && !s.planned && run >= 2 * s.min_steps;
+    if (last_round) {
+      cut_last_round(&s);
+    } else if (a.window < 2560 && 3 * tiles >= s.target) {
+      s.units -= s.target * (s.crowded ? 2 : 1);
+      s.target = s.crowded = s.planned = 0;
+    }
   }
   auto fits = [&] { return s.target == 0 || bytes >= workspace_bytes(s, a.c.heads, a.c.C, a.r.batch); };
   if (s.crowded && !fits()) {            // a workspace made for a larger call may have room for fewer cuts

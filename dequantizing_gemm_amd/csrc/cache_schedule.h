@@ -13,7 +13,9 @@
 // 128: 260 us uncut, 237 so).
 // So cuts add at most `target` blocks, and a tile of c > 1 chunks adds
 // c - 1 >= c / 2 of them, or the blocks are at most 3 target: that bounds the grid
-// and the number of partial results, which the host has to know.
+// and the number of partial results, which the host has to know. Prompts with a window
+// and first tokens, tiles of about one length, have only those of the last round cut
+// (last_round; at most `target` blocks more, and as many partial results).
 #pragma once
 
 #include "cache.h"
@@ -32,6 +34,7 @@ struct Schedule {
   int crowded;                           // tiles may be more than the target by up to half
   int planned;                           // the blocks of each sequence are counted by a kernel of its own
   int partial;                           // every block leaves a partial result, whole tiles too, where tokens are shared
+  int last_round;                        // only the tiles that are left when all places have one as often as they can are cut
 };
 
 // From more sequences than a wavefront looks through at once, their blocks are
@@ -132,6 +135,27 @@ __host__ __device__ inline int steps_per_block(const Schedule& s, float work, fl
     else from = per + 1;
   }
   return from;
+}
+
+// With last_round: the chunks of each tile of the last round, of `tiles` in all of up to
+// `most` steps, as many as the places take, at most `target` of them; and what block `unit`
+// of a head takes. Slots are those of the last round.
+struct UnitShare {
+  int tile, chunk, chunks, slot;         // tile: of all
+};
+__host__ __device__ inline int last_round_chunks(const Schedule& s, int tiles, int most) {
+  const int left = tiles % s.target, fit = left > 0 ? s.target / left : 1, steps = most / s.min_steps;
+  return fit < steps ? fit : steps > 1 ? steps : 1;
+}
+__host__ __device__ inline UnitShare last_round_share(const Schedule& s, int tiles, int chunks, int unit) {
+  const int whole = tiles - tiles % s.target, more = unit - whole;
+  if (more < 0) return UnitShare{unit, 0, 1, 0};
+  return UnitShare{whole + more / chunks, more % chunks, chunks, more};
+}
+inline void cut_last_round(Schedule* s) {
+  s->units -= s->crowded ? s->target : 0;
+  s->crowded = 0;
+  s->last_round = 1;
 }
 
 // Keys [lo, hi) that row `token` of a sequence's rows sees; with a window also those
@@ -259,7 +283,7 @@ struct Workspace {
 __host__ __device__ inline int64_t partial_floats(int tile_rows, int C) { return (int64_t)tile_rows * (32 * C + 2); }
 
 __host__ __device__ inline int workspace_slots(const Schedule& s) {
-  return s.partial ? s.units : (s.crowded ? 3 : 2) * s.target;
+  return s.partial ? s.units : (s.crowded ? 3 : s.last_round ? 1 : 2) * s.target;
 }
 
 inline int64_t workspace_bytes(const Schedule& s, int heads, int C, int batch) {

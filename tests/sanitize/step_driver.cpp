@@ -308,9 +308,44 @@ static void entry_points() {
   CHECK(attend(4, I, 9, P, 256) == INT4DQ_OK && calls == 4 && shared_calls == 2, "no rows");
 }
 
+// Only the last round's tiles cut: each tile in as many blocks as it has chunks, all of
+// them in the grid, and the cut ones' partial results in the workspace.
+static void last_round() {
+  for (int trial = 0; trial < 3000; ++trial) {
+    Schedule s{};
+    s.tile_rows = kWideRows;
+    s.target = (int)pick(1, 40);
+    s.min_steps = pick(0, 1) ? 8 : 16;
+    s.crowded = (int)pick(0, 1);
+    const int tiles = (int)pick(0, 4 * s.target), most = (int)pick(0, 100);
+    s.units = s.target * (s.crowded ? 2 : 1) + tiles + (int)pick(0, 3);
+    cut_last_round(&s);
+    const int chunks = last_round_chunks(s, tiles, most), left = tiles % s.target;
+    CHECK(chunks >= 1 && (chunks == 1 || (chunks - 1) * s.min_steps < most) && left * chunks <= workspace_slots(s), "chunks of the last round");
+    std::vector<std::vector<int>> seen(tiles);
+    std::vector<int> slots(workspace_slots(s));
+    for (int unit = 0; unit < s.units; ++unit) {
+      const UnitShare x = last_round_share(s, tiles, chunks, unit);
+      if (x.tile < 0 || x.tile >= tiles) continue;         // the kernel finds no sequence with it
+      CHECK(x.chunk >= 0 && x.chunk < x.chunks && (x.chunks == 1 || x.chunks == chunks), "chunk");
+      seen[x.tile].resize(x.chunks);
+      ++seen[x.tile][x.chunk];
+      if (x.chunks > 1) {
+        CHECK(x.slot >= 0 && x.slot < left * chunks && slots[x.slot]++ == 0, "a slot of its own");
+        CHECK(x.slot % x.chunks == x.chunk, "a tile's slots side by side");
+      }
+    }
+    for (int t = 0; t < tiles; ++t) {
+      CHECK((int)seen[t].size() == (t < tiles - left ? 1 : chunks), "all of a tile's chunks");
+      for (const int n : seen[t]) CHECK(n == 1, "each chunk once");
+    }
+  }
+}
+
 int main() {
   entry_points();
   pages();
+  last_round();
   attention();
   senseless();
   if (failures) return 1;

@@ -65,6 +65,53 @@ def test_shared_out_over_blocks(dq, lengths, new):
         check(dq, m, table, lengths, starts, q, F16, window, sinks, cache=cache)
 
 
+class Prompts(Sinks):
+    """The model with all rows of a sequence and head at once, for prompts that it would take minutes
+    for row by row; its bounds (cache_model.Model.attend) are those of the worst visible key likewise."""
+
+    def attend(self, q, table, lengths, starts, scale, causal=True, window=0):
+        m, D = self.model, q.shape[2]
+        q = q.astype(np.float64)
+        out, lse = np.zeros(q.shape), np.zeros(q.shape[:2])
+        tol, ltol = np.zeros(q.shape), np.zeros(q.shape[:2])
+        for b, n in enumerate(lengths):
+            got = [[m.values(s, table[b, j // m.S], j % m.S) for j in range(n)] for s in "kv"]
+            k, v = (np.array([x[0] for x in g], np.float64) for g in got)
+            ks, vs = (np.array([x[1] for x in g], np.float64).reshape(n, m.H, D) for g in got)
+            rows = np.arange(starts[b], starts[b + 1])
+            pos, js = (n - len(rows) + rows - rows[0])[:, None], np.arange(n)
+            see = (js <= pos) & ((js > pos - window) | (js < self.sinks))
+            count = see.sum(1)[:, None]
+            for h in range(q.shape[1]):
+                kh, x = h // (q.shape[1] // m.H), q[rows, h]
+                a = np.where(see, x @ k[:, kh].T * scale, -np.inf)
+                top = a.max(1, keepdims=True)
+                p = np.exp(a - top)
+                w = p / p.sum(1, keepdims=True)
+                out[rows, h], lse[rows, h] = w @ v[:, kh], top[:, 0] + np.log(p.sum(1))
+                delta = np.where(see, scale * 2.0 ** -24 * (D + 16) * 16 * (np.abs(x) @ ks[:, kh].T)
+                                 + 2.0 ** -22 * np.abs(np.where(see, a, 0)), 0).max(1, keepdims=True)
+                tol[rows, h] = ((2.0 ** -11 + 2 * delta + 2.0 ** -20) * (w @ np.abs(v[:, kh]))
+                                + (count / 32 + 64) * 2.0 ** -24 * 15 * (w @ vs[:, kh])
+                                + 2.0 ** -24 * np.where(see, vs[:, kh].max(1), 0).max(1, keepdims=True))
+                ltol[rows, h] = delta[:, 0] + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse[rows, h])
+        return out, lse, np.ones(len(q), bool), tol, ltol
+
+
+@pytest.mark.parametrize("lengths,new", [([1800, 1500], [600, 520]), ([1300, 1400, 1250], [500, 900, 700])])
+def test_last_round(dq, lengths, new):
+    """Prompts of a few more tiles than the GPU has places: 35 and 66 on 32 of 16 heads. Those of the
+    last round are cut, unless the workspace has no room for it or the window is short."""
+    rng = np.random.default_rng(sum(lengths))
+    m, table, starts = filled(rng, 16, 64, 64, False, 64, lengths, new)
+    q = rounded(rng.normal(size=(int(starts[-1]), 64, 64)).astype(np.float32), F16)
+    cache = cache_of(dq, m)
+    for window, sinks, kw in ((1100, 70, {}), (1100, 70, dict(workspace=torch.empty(0, dtype=torch.uint8, device=DEV))),
+                              (300, 10, {})):
+        say("case: last round", lengths, new, window, sinks, list(kw))
+        check_attention(dq, Prompts(m, sinks), table, lengths, starts, q, F16, window=window, sinks=sinks, cache=cache, **kw)
+
+
 def test_large_batch(dq):
     """More sequences than a wavefront looks through at once."""
     rng = np.random.default_rng(33)
