@@ -94,31 +94,42 @@ __device__ __forceinline__ Quantised<C> quantise(const CacheView& c, int a, V va
     const uint32_t zp = AFF ? affine_zp(bottom, sf) : 0u;
     q.scale[i] = __builtin_bit_cast(uint16_t, s16);
     q.zero[i] = (uint8_t)zp;
-    // code_of / affine_code of the 8 channels, with one branch around the divisions
-    float code[8];
-    bool near = false;
+    // code_of / affine_code of the 8 channels, with one branch around the divisions. As
+    // code + 8 (affine: the code) on top of kOne, whose unit in the last place is 1, the sum
+    // rounds to the code, and the 8 patterns can be added up, each 4 bits higher, with what
+    // kOne adds to them taken off at the end. Clamped before, which is the same outside
+    // the range; ties, rounded to even of the sum, are among those near a half. (Against
+    // rounding, clamping, converting and shifting each: 28114 tokens, 8 heads of 128,
+    // bfloat16, 39 -> 37.7 us, with zero points in groups of 32 54.9 -> 49.)
+    constexpr float kOne = 0x1.8p23f;
+    constexpr uint32_t kOnes = 0x11111111u * 0x4B400000u;
+    const float base = AFF ? kOne + (float)zp : kOne + 8.0f;
+    const float least = AFF ? -(float)zp : -8.0f, most = AFF ? 15.0f - (float)zp : 7.0f;
+    float code[8], far = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float t = value(i, e) * rsf, n = __builtin_rintf(t);
-      near |= __builtin_fabsf(__builtin_fabsf(t - n) - 0.5f) < 0x1p-14f;         // near_half_integer(t)
-      code[e] = AFF ? __builtin_fminf(__builtin_fmaxf(n + (float)zp, 0.0f), 15.0f)
-                    : __builtin_fminf(__builtin_fmaxf(n, -8.0f), 7.0f);
+      const float t = __builtin_amdgcn_fmed3f(value(i, e) * rsf, least, most);
+      code[e] = base + t;
+      far = __builtin_fmaxf(far, __builtin_fabsf(t - (code[e] - base)));
     }
-    if (__builtin_expect(near, 0)) {
+    if (__builtin_expect(far > 0.5f - 0x1p-14f, 0)) {            // near_half_integer of one of them
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float x = value(i, e);
         if (near_half_integer(x * rsf))
-          code[e] = AFF ? (float)affine_code(x, sf, rsf, zp)
-                        : __builtin_fminf(__builtin_fmaxf(__builtin_rintf(x / sf), -8.0f), 7.0f);   // IEEE division
+          code[e] = AFF ? kOne + (float)affine_code(x, sf, rsf, zp)
+                        : base + __builtin_fminf(__builtin_fmaxf(__builtin_rintf(x / sf), -8.0f), 7.0f);   // IEEE division
       }
     }
     uint32_t word = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t u = (uint32_t)(int)code[e] & 15u;
-      // padding channels have code 0
-      word |= (!AFF || 32 * i + 8 * a + e < c.D ? u : 0u) << (4 * e);
+    for (int e = 7; e >= 0; --e) word = (word << 4) + __builtin_bit_cast(uint32_t, code[e]);
+    word -= kOnes;
+    if constexpr (AFF) {                               // padding channels have code 0
+      const int have = c.D - (32 * i + 8 * a);
+      word &= have >= 8 ? ~0u : have <= 0 ? 0u : (1u << (4 * have)) - 1;
+    } else {
+      word ^= 0x88888888u;
     }
     q.word[i] = word;
   }
