@@ -172,3 +172,63 @@ def test_steps_in_a_graph(dq):
             assert torch.equal(a, b), i
         for name in ("k_packed", "v_packed", "k_scales", "v_scales"):
             assert torch.equal(getattr(cache, name), getattr(twin, name)), name
+
+
+def calls(dq, cache, x, table, lengths, starts, w, rope, shared):
+    """Append, read back, attend in each form."""
+    q, k, v = x
+    q = dq.int4_cache_append(cache, q, k, v, table, lengths, starts, q_norm=w, k_norm=w, rope=rope)
+    back = dq.int4_cache_read(cache, table, lengths, starts, rows=q.shape[0], dtype=q.dtype)
+    ask = q[-40:].contiguous()
+    few = torch.tensor([0, 20, 40], dtype=torch.int32, device=DEV)
+    return [q, *back, *(dq.int4_cache_attention(a, cache, table, lengths, s, **kw) for a, s in ((q, starts), (ask, few))
+                        for kw in (dict(window=300, sinks=70), dict(shared=shared, share_from=1)))]
+
+
+@pytest.mark.parametrize("rows", [700, 5200])
+def test_far_pages(dq, rows):
+    """Pages past 2^32 bytes of codes: the same bits as on the first ones, row by row and as prompts."""
+    H, HQ, D, S, pages = 8, 32, 128, 64, 140000
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    cache = dq.Int4Cache.empty(pages, S, H, D, 64, True)
+    x = [torch.randn(rows, h, D, device=DEV, generator=g).to(BF16) for h in (HQ, H, H)]
+    w, rope = torch.rand(D, device=DEV, generator=g) + 0.5, dev(rope_table(rows, D))
+    n = torch.tensor([rows - rows // 3, rows // 3], dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, rows - rows // 3, rows], dtype=torch.int32, device=DEV)
+    shared = torch.tensor([2 * S], dtype=torch.int32, device=DEV)
+    each = -(-rows // S)
+    near = torch.arange(2 * each, dtype=torch.int32, device=DEV).view(2, each)
+    near[1, :2] = near[0, :2]
+    same = torch.cat([t[:2 * S] for t in x[1:]], 1).clone()      # the shared tokens' keys and values
+    first = rows - rows // 3
+    for i in (1, 2):
+        x[i][first:first + 2 * S] = same[:, (i - 1) * H:i * H]
+    say("case: far pages", rows)
+    want = calls(dq, cache, x, near, n, starts, w, rope, shared)
+    got = calls(dq, cache, x, pages - 1 - near, n, starts, w, rope, shared)
+    for i, (a, b) in enumerate(zip(want, got)):
+        assert torch.isfinite(a).all() and torch.equal(a, b), i
+
+
+def test_far_rows(dq):
+    """Rows 2^27 elements apart, the last ones past 2^31 elements: the same bits as side by side."""
+    H, HQ, D, S, T = 2, 6, 64, 16, 20
+    big = torch.empty(T << 27, dtype=F16, device=DEV).view(T, 1 << 27)
+    wide = big[:, :(HQ + 2 * H) * D].view(T, HQ + 2 * H, D)
+    wide.copy_(torch.randn(T, HQ + 2 * H, D, device=DEV))
+    w, rope = torch.ones(D, device=DEV), dev(rope_table(64, D))
+    table = torch.arange(8, dtype=torch.int32, device=DEV).view(2, 4)
+    n = torch.tensor([40, 12], dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, 8, 20], dtype=torch.int32, device=DEV)
+    got = []
+    for y in (wide, wide.contiguous()):
+        cache = dq.Int4Cache.empty(8, S, H, D, 32, False)
+        for t in (cache.k_packed, cache.v_packed, cache.k_scales, cache.v_scales):
+            t.zero_()
+        x = y.split([HQ, H, H], 1)
+        say("case: far rows", y.stride())
+        q = dq.int4_cache_append(cache, *x, table, n, starts, q_norm=w, k_norm=w, rope=rope)
+        got.append([q, *dq.int4_cache_read(cache, table, n, starts, rows=T, dtype=F16),
+                    dq.int4_cache_attention(x[0], cache, table, n, starts, window=5, sinks=3)])
+    for i, (a, b) in enumerate(zip(*got)):
+        assert torch.isfinite(a).all() and torch.equal(a, b), i
