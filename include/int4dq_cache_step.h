@@ -130,8 +130,8 @@ int int4_cache_append(const int4_cache_t *cache, const int4_cache_rows_t *rows,
  *           (below 0: none). A sequence sees of them what it sees of its own (all
  *           up to its length, its rows up to their positions). They are read through
  *           the first row of page_table, whatever lengths[0] is, once for all
- *           sequences where that pays, and with a workspace for it. The other entries of page_table that stand for them have to name
- *           the same keys and values.
+ *           sequences where that pays, and with a workspace for it. The other entries
+ *           of page_table that stand for them have to name the same keys and values.
  *   share_from  the least number of shared tokens that are computed once, whatever
  *           it costs; below 0: the library chooses, by the number of sequences and of
  *           their rows. Results may differ in rounding.
