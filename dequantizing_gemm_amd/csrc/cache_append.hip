@@ -8,8 +8,10 @@
 //   y_d = (x_d r) w_d,
 //   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) for each pair (a, b),
 // every product and sum rounded to binary32 by itself. The codes of a key go by the
-// last bit of this where a value lies next to a border between two codes; stated so,
-// and with a sum whose order does not show in binary32, they can be reproduced.
+// last bit of this where a value lies next to a border between two codes: the squares are
+// summed in one order in all forms, 8 channels one after the other and then in pairs, so
+// that a code does not depend on the call that wrote it. (Before it is rounded, r is that of
+// the binary64 sum within 2^-52; another order of the sum can give another last bit of r.)
 //
 // Work. L lanes (8, 16 or 32) take a row's head, 8 channels each: 16 bytes a load, the
 // sum over the lanes by DPP, the partner of a channel from the lane that has it, and one

@@ -39,12 +39,20 @@ __device__ __forceinline__ void transform_key(const AppendArgs& a, const AppendP
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[i][e] = value_of<DT>(x.raw[i][e]);
   if (a.k_norm) {
-    double sum = 0.0;
+    // in the order of cache_append.hip: 8 channels one after the other, then block by block
+    // the four threads as four of its lanes, then the blocks pair by pair as its other steps
+    double sum[8] = {};
 #pragma unroll
-    for (int i = 0; i < C; ++i)
+    for (int i = 0; i < C; ++i) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)y[i][e], (double)y[i][e], sum);
-    const float r = norm_factor(lanes_sum<4>(sum) * p.mean + a.eps);
+      for (int e = 0; e < 8; ++e) sum[i] = __builtin_fma((double)y[i][e], (double)y[i][e], sum[i]);
+      sum[i] = lanes_sum<4>(sum[i]);
+    }
+#pragma unroll
+    for (int n = 4; n >= 1; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) sum[i] = sum[2 * i] + sum[2 * i + 1];         // (0 past C: the same)
+    const float r = norm_factor(sum[0] * p.mean + a.eps);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int d = 32 * i + 8 * lane4;
