@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kThreads) void cache_extend_kernel(PagesArgs a, con
                                                                 int64_t* slots, int64_t rows) {
   __shared__ BlockScan scan_rows, scan_pages;
   __shared__ int64_t first_page[kThreads], first_row[kThreads];
-  __shared__ int64_t length_of[kThreads], held_of[kThreads];
+  __shared__ int64_t first_pos[kThreads], held_of[kThreads];
   const int tid = threadIdx.x;
   const int64_t left = a.free_pages(a.count[0]);
   int64_t row0 = 0, page0 = 0;           // rows and pages of the sequences before these
@@ -130,17 +130,17 @@ __global__ __launch_bounds__(kThreads) void cache_extend_kernel(PagesArgs a, con
       if (length < 0) length = 0;
       if (more < 0) more = 0;
     }
-    const int64_t held = a.entries(length), need = a.entries(length + more) - held;
+    const int64_t total = clamp32(length + more), held = a.entries(length), need = a.entries(total) - held;
     int64_t rows_before, rows_all, before, all;
     block_scan(scan_rows, turn, more, &rows_before, &rows_all);
     block_scan(scan_pages, turn, need, &before, &all);
     if (b < a.batch) {
-      a.new_lengths[b] = clamp32(length + more);
+      a.new_lengths[b] = (int32_t)total;
       starts[b] = clamp32(row0 + rows_before);
     }
     first_page[tid] = before;
     first_row[tid] = rows_before;
-    length_of[tid] = length;
+    first_pos[tid] = total - more;       // length, but where the sequence ends at 2^31 - 1
     held_of[tid] = held;
     __syncthreads();
     for (int64_t i = tid; i < all; i += kThreads) {
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void cache_extend_kernel(PagesArgs a, con
       const int64_t end = row0 + rows_all < rows ? rows_all : rows - row0;
       for (int64_t i = tid; i < end; i += kThreads) {
         const int s = last_upto(first_row, kThreads, i);
-        const int64_t pos = length_of[s] + (i - first_row[s]), index = pos >> a.page_shift;
+        const int64_t pos = first_pos[s] + (i - first_row[s]), index = pos >> a.page_shift;
         const int64_t page = index < a.max_pages ? a.table[(int64_t)(b0 + s) * a.table_stride + index] : -1;
         slots[row0 + i] = slot_of(pos, a.page_shift, page, a.pages);
       }
@@ -171,8 +171,10 @@ __global__ __launch_bounds__(kThreads) void cache_extend_kernel(PagesArgs a, con
   }
 }
 
-// A thread a row; lengths and starts are the new ones.
-__global__ __launch_bounds__(256) void cache_slots_kernel(PagesArgs a, const int32_t* starts, int64_t* slots, int64_t rows) {
+// A thread a row; lengths and starts are the new ones. (Positions go by the new tokens, not
+// by the next sequence's start, which may have been clamped.)
+__global__ __launch_bounds__(256) void cache_slots_kernel(PagesArgs a, const int32_t* added, const int32_t* starts,
+                                                          int64_t* slots, int64_t rows) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (t >= rows) return;
   int lo = 0, hi = a.batch;              // the last sequence that starts at or before t
@@ -182,7 +184,8 @@ __global__ __launch_bounds__(256) void cache_slots_kernel(PagesArgs a, const int
   }
   int64_t slot = -1;
   if (t < starts[a.batch]) {
-    const int64_t pos = (int64_t)a.new_lengths[lo] - (starts[lo + 1] - t), index = pos >> a.page_shift;
+    const int64_t more = added ? added[lo] : 1;
+    const int64_t pos = a.new_lengths[lo] - more + (t - starts[lo]), index = pos >> a.page_shift;
     if (pos >= 0 && index < a.max_pages)
       slot = slot_of(pos, a.page_shift, a.table[(int64_t)lo * a.table_stride + index], a.pages);
   }
@@ -209,8 +212,8 @@ hipError_t launch_cache_extend(const PagesArgs& a, const int32_t* added, int32_t
   else
     hipLaunchKernelGGL(cache_extend_kernel<false>, dim3(1), dim3(kThreads), 0, stream, a, added, starts, slots, rows);
   if (apart)
-    hipLaunchKernelGGL(cache_slots_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, stream, a, starts, slots,
-                       rows);
+    hipLaunchKernelGGL(cache_slots_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, stream, a, added, starts,
+                       slots, rows);
   return hipGetLastError();
 }
 

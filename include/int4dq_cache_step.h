@@ -63,12 +63,13 @@ int int4_cache_release(const int4_cache_pool_t *pool, const int32_t *lengths, co
  *   page_table out: the entries that the new tokens need beyond those held, taken
  *              from the free pages in the order of the sequences and of their table
  *              rows; -1 where these run out. Tokens past max_pages pages get none.
- *   new_lengths out: [batch] lengths + added, at most 2^31-1; may be lengths.
+ *   new_lengths out: [batch] lengths + added, at most 2^31-1, which a caller keeps
+ *              below: from there on the new rows have the last positions. May be lengths.
  *   starts     out: [batch + 1] exclusive sums of added: the rows of each sequence
  *              as int4dq_cache.h has them.
  *   slots      out: [rows], or NULL: for each row page * page_size + the place on
- *              the page of its token, -1 where it has no page and behind the last
- *              sequence's rows.
+ *              the page of its position, as the other calls derive it from new_lengths
+ *              and starts, -1 where it has no page and behind the last sequence's rows.
  *   new_count  out: [2] the free pages, and how many more were needed; may be count.
  * Errors: those of int4_cache_release, and EINVAL for rows outside 0 .. 2^26.
  */
