@@ -170,6 +170,23 @@ def _rows_of(cache, index, t, name, heads):
     raise ValueError(_rows_array(cache, t, name, heads))         # (which says what is wrong)
 
 
+def _rope(rope, index):
+    """Address, row stride, positions and rotated channels of a table of cosines and sines, or of none."""
+    if rope is None:
+        return None, 0, 0, 0
+    if not isinstance(rope, _Tensor) or rope.dtype is not torch.float32 or rope.dim() != 2:
+        raise ValueError("rope must be a float32 tensor of 2 dimensions")
+    if rope.get_device() != index:
+        raise ValueError(f"rope must be on cuda:{index} (got {rope.device})")
+    positions, rotary = rope.shape
+    if positions < 1 or rotary < 2:            # a tensor without elements has no address, which would mean no rotation
+        raise ValueError(f"rope must have a position and a pair of channels at least (got {tuple(rope.shape)})")
+    row, channel = rope.stride()
+    if channel != 1:
+        raise ValueError("rope must be contiguous in its last dimension")
+    return rope.data_ptr(), row if positions > 1 else rotary, positions, rotary
+
+
 def int4_cache_append(cache: Int4Cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
                       lengths: torch.Tensor, starts: torch.Tensor | None = None, *, q_norm: torch.Tensor | None = None,
                       k_norm: torch.Tensor | None = None, eps: float = 1e-6, rope: torch.Tensor | None = None,
@@ -204,19 +221,7 @@ def int4_cache_append(cache: Int4Cache, q: torch.Tensor, k: torch.Tensor, v: tor
     plan = _RowsStruct(at, stride, max_pages, n, s, batch, rows)
     qw = None if q_norm is None else _vector(q_norm, "q_norm", torch.float32, cache.head_dim, index)
     kw = None if k_norm is None else _vector(k_norm, "k_norm", torch.float32, cache.head_dim, index)
-    if rope is None:
-        transform = _TransformStruct(qw, kw, eps, None, 0, 0, 0, bool(interleaved))
-    else:
-        if not isinstance(rope, _Tensor) or rope.dtype is not torch.float32 or rope.dim() != 2:
-            raise ValueError("rope must be a float32 tensor of 2 dimensions")
-        if rope.get_device() != index:
-            raise ValueError(f"rope must be on {cache.device} (got {rope.device})")
-        positions, rotary = rope.shape
-        row, channel = rope.stride()
-        if channel != 1 and rotary > 1:
-            raise ValueError("rope must be contiguous in its last dimension")
-        transform = _TransformStruct(qw, kw, eps, rope.data_ptr(), row if positions > 1 else rotary, positions, rotary,
-                                     bool(interleaved))
+    transform = _TransformStruct(qw, kw, eps, *_rope(rope, index), bool(interleaved))
     if out is None:
         out = q.new_empty(q.shape)
     else:
