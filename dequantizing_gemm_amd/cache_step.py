@@ -140,7 +140,11 @@ def int4_cache_extend(page_table: torch.Tensor, lengths: torch.Tensor, free: tor
     or more, known to the caller) the slot page * page_size + offset of its token, int64,
     -1 where it has none (None with ``slots=False``); and the free pages with how many
     more were needed. ``out``: the four to fill, of which the first and last may be
-    ``lengths`` and ``count``."""
+    ``lengths`` and ``count``.
+
+    A token that lacks a page has none later either. To take such a step back, keep
+    ``lengths`` and ``count`` (no ``out``), give pages back with int4_cache_release on
+    them, and call again with what that returns."""
     pool, index, batch, n, c = _pool(page_table, lengths, free, count, page_size)
     added = None if new is None else _vector(new, "new", _int32_type, batch, index)
     if rows is None:

@@ -71,6 +71,11 @@ int int4_cache_release(const int4_cache_pool_t *pool, const int32_t *lengths, co
  *              the page of its position, as the other calls derive it from new_lengths
  *              and starts, -1 where it has no page and behind the last sequence's rows.
  *   new_count  out: [2] the free pages, and how many more were needed; may be count.
+ * An entry of -1 counts as held, so that a token that lacks a page has none later either.
+ * A caller who does not want that takes the step back where new_count[1] is above 0: the
+ * call leaves free, and lengths and count where they are not its outputs, as they were;
+ * with these, pages given back by int4_cache_release, and the call once more, the table's
+ * entries are written anew.
  * Errors: those of int4_cache_release, and EINVAL for rows outside 0 .. 2^26.
  */
 int int4_cache_extend(const int4_cache_pool_t *pool, const int32_t *lengths, const int32_t *added,
