@@ -308,9 +308,10 @@ def int4_cache_attention(q: torch.Tensor, cache: Int4Cache, page_table: torch.Te
 
     ``sinks``: with a window, the first ``sinks`` tokens stay visible too. ``shared``
     int32 [1] on the GPU: all sequences begin with the same shared[0] tokens, which
-    are then read once for all of them where that pays (or from ``share_from`` tokens
-    on), through the first row of ``page_table``; the result is what it is without, but
-    for rounding."""
+    are then read once for all of them, through the first row of ``page_table``, from
+    ``share_from`` tokens on; the result is what it is without, but for rounding. By default
+    the library chooses that number, by the sequences and their rows and not by the
+    window: with a window that reaches few of the shared tokens, leave ``shared`` out."""
     _is_cache(cache)
     q_heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
     qs = _rows_array(cache, q, "q", q_heads)

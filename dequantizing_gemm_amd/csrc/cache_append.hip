@@ -23,8 +23,8 @@
 //
 // What bounds long prompts (28114 tokens of 8 + 32 heads of 128, bfloat16, symmetric codes
 // in groups of 128): the queries memory, 460 MB in 101 us, 4.6 TB/s; keys and values the
-// latency of their loads and the VALU (busy for half of 74 us): a block is 64 tokens of
-// one head, and four wavefronts a SIMD is what its 114 registers leave. Both in one
+// latency of their loads and the VALU (busy for half of 73 us): a block is 64 tokens of
+// one head, and four wavefronts a SIMD is what its 122 registers leave. Both in one
 // launch with their blocks in turns took 187 us, one after the other 175. Summing in
 // binary64 costs nothing that shows (without norms 154 us, without rotation 147 of 175).
 #include "cache_append.h"

@@ -26,6 +26,14 @@ struct Parts {
 //    519 and 510 with 8192; 16 of 16 to 64 rows 330 and 368, 182 and 177; but 4 of 30 to 250
 //    rows 434 and 417, 16 of 100 to 500 2108 and 1999, 16 of 4 rows each, whose tiles are
 //    full, 68 and 58.
+//  - What this rule leaves to share_from: many sequences with full tiles, for which the
+//    shared part's tiles of 128 rows of the whole batch take codes apart less often. 64 of
+//    one row with 16 query heads a key head (4 of these) 123 and 150 us with 32768 shared
+//    tokens, 59 and 48 with 8192; 128 of 4 rows 374 and 543, with 4096 104 and 102; 32 of 4
+//    rows 132 and 146; 128 of 8 rows 699 and 736, 32 of them 206 and 205, 8 of them 75 and 67.
+//  - It does not go by a window, which the shared part's cut does not know either, so that
+//    a short one loses: 64 sequences of 10 to 1500 own tokens on 32768, window 1000, 44 and
+//    24 us, 2048 47 and 33, 8192 57 and 84, 40000 86 and 354.
 inline int64_t sharing_pays(const RowsView& r, int ratio) {
   const int64_t rows = r.rows * ratio, tokens = 24576 / (r.batch > 0 ? r.batch : 1);
   if (rows <= 8 * (int64_t)r.batch) return r.batch < 4 ? 0 : tokens > 1536 ? tokens : 1536;

@@ -136,11 +136,15 @@ int int4_cache_append(const int4_cache_t *cache, const int4_cache_rows_t *rows,
  *           (below 0: none). A sequence sees of them what it sees of its own (all
  *           up to its length, its rows up to their positions). They are read through
  *           the first row of page_table, whatever lengths[0] is, once for all
- *           sequences where that pays, and with a workspace for it. The other entries
+ *           sequences from share_from on, and with a workspace for it. The other entries
  *           of page_table that stand for them have to name the same keys and values.
  *   share_from  the least number of shared tokens that are computed once, whatever
  *           it costs; below 0: the library chooses, by the number of sequences and of
- *           their rows. Results may differ in rounding.
+ *           their rows: from 1536 to 6144 tokens on for 4 or more sequences of up to 8 query
+ *           rows to a key head, from 16384 on for 8 or more of 65 to 640 (16384 in all),
+ *           otherwise not at all. It does not go by the window: with one that reaches
+ *           few of the shared tokens a call without `shared` is faster. Results may differ
+ *           in rounding.
  *   The arithmetic is that of int4_cache_attention; with shared tokens the two parts
  *   of a row are joined in binary32.
  * Errors: those of int4_cache_attention, and EINVAL for sinks < 0.
