@@ -171,8 +171,8 @@ __global__ __launch_bounds__(kThreads) void cache_extend_kernel(PagesArgs a, con
   }
 }
 
-// A thread a row; lengths and starts are the new ones. (Positions go by the new tokens, not
-// by the next sequence's start, which may have been clamped.)
+// A thread a row; lengths and starts are the new ones. (The new tokens are read themselves only
+// where starts do not tell them: their array may be that of the lengths, which are new by now.)
 __global__ __launch_bounds__(256) void cache_slots_kernel(PagesArgs a, const int32_t* added, const int32_t* starts,
                                                           int64_t* slots, int64_t rows) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(256) void cache_slots_kernel(PagesArgs a, const int
   }
   int64_t slot = -1;
   if (t < starts[a.batch]) {
-    const int64_t more = added ? added[lo] : 1;
+    const int64_t more = starts[lo + 1] < INT32_MAX || !added ? starts[lo + 1] - starts[lo] : added[lo];
     const int64_t pos = a.new_lengths[lo] - more + (t - starts[lo]), index = pos >> a.page_shift;
     if (pos >= 0 && index < a.max_pages)
       slot = slot_of(pos, a.page_shift, a.table[(int64_t)lo * a.table_stride + index], a.pages);

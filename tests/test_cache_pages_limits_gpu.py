@@ -78,3 +78,20 @@ def test_ends_of_sequences(dq, lengths, added):
     _, count = dq.int4_cache_release(t, n, f, c, S, done)
     assert count.tolist() == [pages, 0]
     assert sorted(f.tolist()) == list(range(pages))
+
+
+@pytest.mark.parametrize("rows", [600, 5000])
+def test_as_many_new_tokens_as_there_were(dq, rows):
+    """Lengths that are the new tokens too, and are written in place."""
+    n, batch, page = i32([rows // 4 + 7, 0, rows // 4 - 7, rows // 2]), 4, 16
+    most = -(-rows // page) + 1
+    before = n.tolist()
+    table = torch.arange(batch * most, dtype=torch.int32, device=DEV).view(batch, most)
+    free = torch.arange(batch * most, dtype=torch.int32, device=DEV)
+    want = [t.clone() for t in dq.int4_cache_extend(table.clone(), n, free, i32([batch * most, 0]), page, n.clone(), rows=rows)]
+    starts, slots, count = i32([0] * 5), torch.zeros(rows, dtype=torch.int64, device=DEV), i32([batch * most, 0])
+    print("case: doubled", rows, flush=True)
+    got = dq.int4_cache_extend(table, n, free, count, page, n, rows=rows, out=(n, starts, slots, count))
+    assert got[0].tolist() == [2 * x for x in before]
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
